@@ -7,9 +7,12 @@ HIP stream. Every step of the computation runs in the library's kernels.
 There is no fallback: if the library is missing, importing the binding
 raises.
 
-The five ops follow the per-step calls of "Expert Parallelism: common C API
+The five routing ops follow the per-step calls of "Expert Parallelism: common C API
 + NCCL EP backend" (section "Per-step (allocation-free, CUDA-graph
-capturable)"): prepare, dispatch, combine, dispatch_bwd and combine_bwd.
+capturable)"): prepare, dispatch, combine, dispatch_bwd and combine_bwd. The
+experts' own work between dispatch and combine stands beside them: the grouped
+linear, its backward and its 4-bit form, and the gated activation with its
+backward.
 """
 from __future__ import annotations
 
@@ -52,7 +55,9 @@ _CODE_OF = {torch.bfloat16: DTYPE_BF16, torch.float16: DTYPE_FP16, torch.float32
 ENTRY_POINTS = ("ep_recv_capacity_worst", "ep_handle_mem_size", "ep_handle_regions",
                 "ep_prepare", "ep_prepare_static", "ep_dispatch",
                 "ep_combine", "ep_dispatch_bwd", "ep_combine_bwd", "ep_combine_weighted",
-                "ep_combine_weighted_bwd", "ep_read_status", "ep_status_str")
+                "ep_combine_weighted_bwd", "ep_grouped_linear", "ep_grouped_linear_bwd",
+                "ep_grouped_linear_quant", "ep_swiglu", "ep_swiglu_bwd", "ep_read_status",
+                "ep_status_str")
 
 
 class Layout(C.Structure):
@@ -139,10 +144,16 @@ def _load_library(path: str = LIB_PATH):
     lib.ep_combine_weighted.argtypes = [lp, vp, sz, vp, vp, vp, vp]
     lib.ep_combine_weighted_bwd.argtypes = [lp, vp, sz, vp, vp, vp, vp, vp, vp]
     lib.ep_read_status.argtypes = [vp, C.POINTER(C.c_uint32), vp]
+    lib.ep_grouped_linear.argtypes = [lp, vp, sz, vp, vp, vp, i64, vp]
+    lib.ep_grouped_linear_bwd.argtypes = [lp, vp, sz, vp, vp, vp, vp, vp, i64, vp]
+    lib.ep_grouped_linear_quant.argtypes = [lp, vp, sz, vp, vp, vp, vp, vp, i64, i32, vp]
+    lib.ep_swiglu.argtypes = [lp, vp, sz, vp, vp, vp]
+    lib.ep_swiglu_bwd.argtypes = [lp, vp, sz, vp, vp, vp, vp]
     for name in ("ep_prepare", "ep_prepare_static", "ep_dispatch", "ep_combine",
                  "ep_dispatch_bwd",
                  "ep_combine_bwd", "ep_combine_weighted", "ep_combine_weighted_bwd",
-                 "ep_read_status"):
+                 "ep_grouped_linear", "ep_grouped_linear_bwd", "ep_grouped_linear_quant",
+                 "ep_swiglu", "ep_swiglu_bwd", "ep_read_status"):
         getattr(lib, name).restype = C.c_int
     lib.ep_status_str.argtypes = [C.c_int]
     lib.ep_status_str.restype = C.c_char_p
@@ -220,6 +231,12 @@ def _need(t: Optional[torch.Tensor], name: str, dtype, shape=None, allow_none=Fa
         raise ValueError(f"{name} must be contiguous")
     if shape is not None and tuple(t.shape) != tuple(shape):
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+
+
+def _out_features(weight: torch.Tensor) -> int:
+    if weight.dim() != 3:
+        raise ValueError(f"weight must have shape (E, N, H), got {tuple(weight.shape)}")
+    return weight.shape[1]
 
 
 def new_handle(layout: Layout, device=None) -> torch.Tensor:
@@ -330,6 +347,85 @@ def combine_weighted_bwd(layout: Layout, handle: torch.Tensor, grad: torch.Tenso
                                        _ptr(grad), _ptr(expert_out), _ptr(recv_topk_weights),
                                        _ptr(grad_expert_out), _ptr(grad_recv_topk_weights),
                                        _stream(stream)), "ep_combine_weighted_bwd")
+
+
+def grouped_linear(layout: Layout, handle: torch.Tensor, x: torch.Tensor, weight: torch.Tensor,
+                   out: torch.Tensor, stream=None):
+    """out [cap,N] = each live row of x [cap,H] through its expert's weight [E,N,H]."""
+    N = _out_features(weight)
+    _need(handle, "handle", torch.uint8)
+    _need(x, "x", layout.payload_dtype, (layout.cap, layout.H))
+    _need(weight, "weight", layout.payload_dtype, (layout.E, N, layout.H))
+    _need(out, "out", layout.payload_dtype, (layout.cap, N))
+    _check(lib.ep_grouped_linear(C.byref(layout), _ptr(handle), handle.numel(), _ptr(x),
+                                 _ptr(weight), _ptr(out), N, _stream(stream)),
+           "ep_grouped_linear")
+
+
+def grouped_linear_bwd(layout: Layout, handle: torch.Tensor, grad: torch.Tensor,
+                       x: Optional[torch.Tensor], weight: Optional[torch.Tensor],
+                       grad_x: Optional[torch.Tensor] = None,
+                       grad_weight: Optional[torch.Tensor] = None, stream=None):
+    """The gradients of ``grouped_linear``; an output that is None is skipped,
+    and so is the operand that only it needs (weight for grad_x, x for
+    grad_weight)."""
+    if grad.dim() != 2:
+        raise ValueError(f"grad must have two dimensions, got {tuple(grad.shape)}")
+    N = grad.shape[1]
+    _need(handle, "handle", torch.uint8)
+    _need(grad, "grad", layout.payload_dtype, (layout.cap, N))
+    _need(x, "x", layout.payload_dtype, (layout.cap, layout.H), allow_none=grad_weight is None)
+    _need(weight, "weight", layout.payload_dtype, (layout.E, N, layout.H),
+          allow_none=grad_x is None)
+    _need(grad_x, "grad_x", layout.payload_dtype, (layout.cap, layout.H), allow_none=True)
+    _need(grad_weight, "grad_weight", layout.payload_dtype, (layout.E, N, layout.H),
+          allow_none=True)
+    _check(lib.ep_grouped_linear_bwd(C.byref(layout), _ptr(handle), handle.numel(), _ptr(grad),
+                                     _ptr(x), _ptr(weight), _ptr(grad_x), _ptr(grad_weight), N,
+                                     _stream(stream)), "ep_grouped_linear_bwd")
+
+
+def grouped_linear_quant(layout: Layout, handle: torch.Tensor, x: torch.Tensor,
+                         qweight: torch.Tensor, scales: torch.Tensor,
+                         zeros: Optional[torch.Tensor], out: torch.Tensor, stream=None):
+    """``grouped_linear`` with 4-bit weights: qweight uint8 [E,N,H/2] (the low
+    four bits are the even input), scales [E,N,H/G] of the payload type, zeros
+    uint8 [E,N,H/G] or None for 8; the group size G follows from the shapes."""
+    if scales.dim() != 3 or scales.shape[2] < 1 or layout.H % scales.shape[2] != 0:
+        raise ValueError(f"scales must have shape (E, N, H / group), got {tuple(scales.shape)}")
+    N, groups = scales.shape[1], scales.shape[2]
+    _need(handle, "handle", torch.uint8)
+    _need(x, "x", layout.payload_dtype, (layout.cap, layout.H))
+    _need(qweight, "qweight", torch.uint8, (layout.E, N, layout.H // 2))
+    _need(scales, "scales", layout.payload_dtype, (layout.E, N, groups))
+    _need(zeros, "zeros", torch.uint8, (layout.E, N, groups), allow_none=True)
+    _need(out, "out", layout.payload_dtype, (layout.cap, N))
+    _check(lib.ep_grouped_linear_quant(C.byref(layout), _ptr(handle), handle.numel(), _ptr(x),
+                                       _ptr(qweight), _ptr(scales), _ptr(zeros), _ptr(out), N,
+                                       layout.H // groups, _stream(stream)),
+           "ep_grouped_linear_quant")
+
+
+def swiglu(layout: Layout, handle: torch.Tensor, gate_up: torch.Tensor, out: torch.Tensor,
+           stream=None):
+    """out [cap,H] = silu(gate) * up of each live row, gate and up the halves
+    of gate_up [cap,2H]."""
+    _need(handle, "handle", torch.uint8)
+    _need(gate_up, "gate_up", layout.payload_dtype, (layout.cap, 2 * layout.H))
+    _need(out, "out", layout.payload_dtype, (layout.cap, layout.H))
+    _check(lib.ep_swiglu(C.byref(layout), _ptr(handle), handle.numel(), _ptr(gate_up),
+                         _ptr(out), _stream(stream)), "ep_swiglu")
+
+
+def swiglu_bwd(layout: Layout, handle: torch.Tensor, grad: torch.Tensor,
+               gate_up: torch.Tensor, grad_gate_up: torch.Tensor, stream=None):
+    _need(handle, "handle", torch.uint8)
+    _need(grad, "grad", layout.payload_dtype, (layout.cap, layout.H))
+    _need(gate_up, "gate_up", layout.payload_dtype, (layout.cap, 2 * layout.H))
+    _need(grad_gate_up, "grad_gate_up", layout.payload_dtype, (layout.cap, 2 * layout.H))
+    _check(lib.ep_swiglu_bwd(C.byref(layout), _ptr(handle), handle.numel(), _ptr(grad),
+                             _ptr(gate_up), _ptr(grad_gate_up), _stream(stream)),
+           "ep_swiglu_bwd")
 
 
 def read_status(handle: torch.Tensor, stream=None) -> int:

@@ -14,11 +14,13 @@ from __future__ import annotations
 import os
 import shutil
 import subprocess
+import tempfile
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
-SOURCES = [os.path.join(CSRC, "ep_api.hip"), os.path.join(CSRC, "ep_kernels.hip")]
+SOURCES = [os.path.join(CSRC, f) for f in ("ep_api.hip", "ep_kernels.hip", "ep_linear.hip",
+                                           "ep_quant.hip", "ep_swiglu.hip")]
 LIB_NAME = "libcombine_ep_prepare_amd.so"
 LIB = os.path.join(HERE, LIB_NAME)
 CEILINGS_SOURCE = os.path.join(CSRC, "ep_ceilings.hip")
@@ -41,13 +43,25 @@ def hipcc() -> str:
 
 
 def _compile(sources, out: str, verbose: bool) -> None:
-    tmp = out + ".tmp"
-    cmd = [hipcc(), *HIPCC_FLAGS, "-I", os.path.join(ROOT, "include"), "-I", CSRC,
-           "-o", tmp, *sources]
-    if verbose:
-        print(" ".join(cmd), flush=True)
-    subprocess.run(cmd, check=True)
-    os.replace(tmp, out)
+    """One object per source, compiled side by side, then one link."""
+    includes = ["-I", os.path.join(ROOT, "include"), "-I", CSRC]
+    compile_flags = [f for f in HIPCC_FLAGS if f != "-shared"]
+    with tempfile.TemporaryDirectory(prefix="ep_build_") as work:
+        objects = [os.path.join(work, os.path.basename(s) + ".o") for s in sources]
+        cmds = [[hipcc(), *compile_flags, *includes, "-c", "-o", o, s]
+                for s, o in zip(sources, objects)]
+        if verbose:
+            for cmd in cmds:
+                print(" ".join(cmd), flush=True)
+        running = [subprocess.Popen(cmd) for cmd in cmds]
+        codes = [p.wait() for p in running]
+        for cmd, code in zip(cmds, codes):
+            if code != 0:
+                raise subprocess.CalledProcessError(code, cmd)
+        tmp = out + ".tmp"
+        subprocess.run([hipcc(), f"--offload-arch={ARCH}", "-shared", "-fPIC", "-o", tmp,
+                        *objects], check=True)
+        os.replace(tmp, out)
 
 
 def build(verbose: bool = False) -> str:

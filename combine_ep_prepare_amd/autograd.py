@@ -28,6 +28,11 @@ row, a reduction over it) therefore gets exact parameter gradients. With
 ``EpRouting(..., zero_tail=False)`` the tail is left unwritten (one zero
 write per tail row saved) and such a function must slice the buffer to its
 live rows first; with ``fill_pads=False`` pad rows are unwritten too.
+
+`grouped_linear`, `swiglu` and `grouped_linear_quant` are the experts' own
+work between dispatch and combine: each expert's weights applied to its
+segment, and the gated activation. They read and write live rows only, so
+they give the same results with either policy.
 """
 from __future__ import annotations
 
@@ -38,7 +43,10 @@ import torch
 from . import (Layout, combine as _combine, combine_bwd as _combine_bwd,
                combine_weighted as _combine_weighted,
                combine_weighted_bwd as _combine_weighted_bwd, dispatch as _dispatch,
-               dispatch_bwd as _dispatch_bwd, new_handle, prepare, recv_capacity_worst)
+               dispatch_bwd as _dispatch_bwd, grouped_linear as _grouped_linear,
+               grouped_linear_bwd as _grouped_linear_bwd,
+               grouped_linear_quant as _grouped_linear_quant, new_handle, prepare,
+               recv_capacity_worst, swiglu as _swiglu, swiglu_bwd as _swiglu_bwd)
 
 
 class EpRouting:
@@ -67,12 +75,16 @@ class EpRouting:
         prepare(self.layout, topk_idx.contiguous(), self.token_counts, self.handle,
                 self.expert_offsets)
 
-    def layout_for(self, dtype: torch.dtype) -> Layout:
-        """The layout of this routing for payloads of ``dtype``."""
-        if dtype not in self._layouts:
-            self._layouts[dtype] = Layout(*self._dims, dtype=dtype, fill_pads=self.fill_pads,
-                                          zero_tail=self.zero_tail)
-        return self._layouts[dtype]
+    def layout_for(self, dtype: torch.dtype, hidden: Optional[int] = None) -> Layout:
+        """The layout of this routing for payloads of ``dtype``, with rows of
+        ``hidden`` elements (the routing's own if not given)."""
+        T, K, E, A, H, cap = self._dims
+        hidden = H if hidden is None else hidden
+        if (dtype, hidden) not in self._layouts:
+            self._layouts[dtype, hidden] = Layout(T, K, E, A, hidden, cap, dtype=dtype,
+                                                  fill_pads=self.fill_pads,
+                                                  zero_tail=self.zero_tail)
+        return self._layouts[dtype, hidden]
 
 
 class _Dispatch(torch.autograd.Function):
@@ -153,6 +165,50 @@ class _CombineWeighted(torch.autograd.Function):
         return grad_rows if want_rows else None, grad_w, None
 
 
+class _GroupedLinear(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, weight, routing: EpRouting):
+        L = routing.layout_for(x.dtype, x.shape[1])
+        x, weight = x.contiguous(), weight.contiguous()
+        out = torch.empty(L.cap, weight.shape[1], dtype=x.dtype, device=x.device)
+        _grouped_linear(L, routing.handle, x, weight, out)
+        ctx.routing = routing
+        ctx.save_for_backward(x, weight)
+        return out
+
+    @staticmethod
+    def backward(ctx, grad):
+        x, weight = ctx.saved_tensors
+        L = ctx.routing.layout_for(x.dtype, x.shape[1])
+        want_x, want_w = ctx.needs_input_grad[0], ctx.needs_input_grad[1]
+        grad_x = torch.empty_like(x) if want_x else None
+        grad_w = torch.empty_like(weight) if want_w else None
+        if want_x or want_w:
+            _grouped_linear_bwd(L, ctx.routing.handle, grad.contiguous(), x, weight, grad_x,
+                                grad_w)
+        return grad_x, grad_w, None
+
+
+class _SwiGLU(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, gate_up, routing: EpRouting):
+        L = routing.layout_for(gate_up.dtype, gate_up.shape[1] // 2)
+        gate_up = gate_up.contiguous()
+        out = torch.empty(L.cap, L.H, dtype=gate_up.dtype, device=gate_up.device)
+        _swiglu(L, routing.handle, gate_up, out)
+        ctx.routing = routing
+        ctx.save_for_backward(gate_up)
+        return out
+
+    @staticmethod
+    def backward(ctx, grad):
+        (gate_up,) = ctx.saved_tensors
+        L = ctx.routing.layout_for(gate_up.dtype, gate_up.shape[1] // 2)
+        grad_gate_up = torch.empty_like(gate_up)
+        _swiglu_bwd(L, ctx.routing.handle, grad.contiguous(), gate_up, grad_gate_up)
+        return grad_gate_up, None
+
+
 def dispatch(tokens: torch.Tensor, topk_weights: torch.Tensor, routing: EpRouting):
     """(recv_tokens [cap,H], recv_topk_weights [cap]); rows past the live total
     are zeros (unless the routing was made with ``zero_tail=False``)."""
@@ -166,3 +222,41 @@ def combine(expert_out: torch.Tensor, routing: EpRouting,
     if recv_topk_weights is None:
         return _Combine.apply(expert_out, routing)
     return _CombineWeighted.apply(expert_out, recv_topk_weights, routing)
+
+
+def _rows(t: torch.Tensor, name: str):
+    if t.dim() != 2:
+        raise ValueError(f"{name} must have two dimensions, got {tuple(t.shape)}")
+
+
+def grouped_linear(x: torch.Tensor, weight: torch.Tensor, routing: EpRouting) -> torch.Tensor:
+    """Each live row of x [cap,H] through its expert's weight [E,N,H]: [cap,N]."""
+    _rows(x, "x")
+    return _GroupedLinear.apply(x, weight, routing)
+
+
+def swiglu(gate_up: torch.Tensor, routing: EpRouting) -> torch.Tensor:
+    """silu(gate) * up of each live row, gate and up the halves of gate_up
+    [cap,2I]: [cap,I]."""
+    _rows(gate_up, "gate_up")
+    return _SwiGLU.apply(gate_up, routing)
+
+
+def grouped_linear_quant(x: torch.Tensor, qweight: torch.Tensor, scales: torch.Tensor,
+                         routing: EpRouting, zeros: Optional[torch.Tensor] = None
+                         ) -> torch.Tensor:
+    """``grouped_linear`` with 4-bit weights (the binding's layout of qweight,
+    scales and zeros). For serving: it has no backward, and refuses inputs
+    that require a gradient."""
+    _rows(x, "x")
+    if torch.is_grad_enabled() and (x.requires_grad or scales.requires_grad):
+        raise RuntimeError("grouped_linear_quant has no backward: call it under torch.no_grad() "
+                           "or on inputs that do not require a gradient")
+    L = routing.layout_for(x.dtype, x.shape[1])
+    if scales.dim() != 3:
+        raise ValueError(f"scales must have shape (E, N, H / group), got {tuple(scales.shape)}")
+    out = torch.empty(L.cap, scales.shape[1], dtype=x.dtype, device=x.device)
+    _grouped_linear_quant(L, routing.handle, x.contiguous(), qweight.contiguous(),
+                          scales.contiguous(), None if zeros is None else zeros.contiguous(),
+                          out)
+    return out

@@ -130,6 +130,10 @@ ep_status_t payload_common(const ep_layout_t* L, const void* handle_mem, size_t 
   return EP_OK;
 }
 
+// Feature counts of the experts' products: a multiple of 8 up to
+// EP_MAX_FEATURES, so that an offset inside one tile of rows fits 32 bits.
+bool features_ok(int64_t n) { return n >= 8 && n % 8 == 0 && n <= EP_MAX_FEATURES; }
+
 }  // namespace
 
 extern "C" {
@@ -349,6 +353,108 @@ ep_status_t ep_combine_weighted_bwd(const ep_layout_t* layout, const void* handl
   if (st != EP_OK) return st;
   if (launch_weighted_bwd(d, hv, grad, expert_out, recv_topk_weights, grad_expert_out,
                           grad_recv_topk_weights, num_cus, stream) != hipSuccess)
+    return EP_ERR_HIP;
+  return EP_OK;
+}
+
+ep_status_t ep_grouped_linear(const ep_layout_t* layout, const void* handle_mem,
+                              size_t handle_bytes, const void* x, const void* weight, void* out,
+                              int64_t out_features, hipStream_t stream) {
+  Dims d;
+  HandleView hv;
+  int num_cus = 0;
+  ep_status_t st = payload_common(layout, handle_mem, handle_bytes, &d, &hv);
+  if (st != EP_OK) return st;
+  if (!features_ok(d.H) || !features_ok(out_features)) return EP_ERR_SHAPE;
+  if (!weight || (d.cap > 0 && (!x || !out))) return EP_ERR_NULL;
+  if (!aligned16(x) || !aligned16(weight) || !aligned16(out)) return EP_ERR_ALIGN;
+  st = current_device(&num_cus);
+  if (st != EP_OK) return st;
+  if (launch_grouped_linear(d, hv, x, weight, out, out_features, num_cus, stream) != hipSuccess)
+    return EP_ERR_HIP;
+  return EP_OK;
+}
+
+ep_status_t ep_grouped_linear_bwd(const ep_layout_t* layout, const void* handle_mem,
+                                  size_t handle_bytes, const void* grad, const void* x,
+                                  const void* weight, void* grad_x, void* grad_weight,
+                                  int64_t out_features, hipStream_t stream) {
+  Dims d;
+  HandleView hv;
+  int num_cus = 0;
+  ep_status_t st = payload_common(layout, handle_mem, handle_bytes, &d, &hv);
+  if (st != EP_OK) return st;
+  if (!features_ok(d.H) || !features_ok(out_features)) return EP_ERR_SHAPE;
+  if (d.cap > 0 && !grad) return EP_ERR_NULL;
+  if (!grad_x && !grad_weight) return EP_ERR_NULL;
+  if (grad_x && !weight) return EP_ERR_NULL;
+  if (grad_weight && d.cap > 0 && !x) return EP_ERR_NULL;
+  if (!aligned16(grad) || !aligned16(x) || !aligned16(weight) || !aligned16(grad_x) ||
+      !aligned16(grad_weight))
+    return EP_ERR_ALIGN;
+  st = current_device(&num_cus);
+  if (st != EP_OK) return st;
+  if (launch_grouped_linear_bwd(d, hv, grad, x, weight, grad_x, grad_weight, out_features,
+                                num_cus, stream) != hipSuccess)
+    return EP_ERR_HIP;
+  return EP_OK;
+}
+
+ep_status_t ep_grouped_linear_quant(const ep_layout_t* layout, const void* handle_mem,
+                                    size_t handle_bytes, const void* x, const uint8_t* qweight,
+                                    const void* scales, const uint8_t* zeros, void* out,
+                                    int64_t out_features, int32_t group_size,
+                                    hipStream_t stream) {
+  Dims d;
+  HandleView hv;
+  int num_cus = 0;
+  ep_status_t st = payload_common(layout, handle_mem, handle_bytes, &d, &hv);
+  if (st != EP_OK) return st;
+  if (!features_ok(d.H) || !features_ok(out_features)) return EP_ERR_SHAPE;
+  if (d.dtype == EP_DTYPE_FP32) return EP_ERR_SHAPE;
+  if ((group_size != 32 && group_size != 64 && group_size != 128) || d.H % group_size != 0)
+    return EP_ERR_SHAPE;
+  if (!qweight || !scales || (d.cap > 0 && (!x || !out))) return EP_ERR_NULL;
+  if (!aligned16(x) || !aligned16(qweight) || !aligned16(scales) || !aligned16(zeros) ||
+      !aligned16(out))
+    return EP_ERR_ALIGN;
+  st = current_device(&num_cus);
+  if (st != EP_OK) return st;
+  if (launch_grouped_quant(d, hv, x, qweight, scales, zeros, out, out_features, group_size,
+                           num_cus, stream) != hipSuccess)
+    return EP_ERR_HIP;
+  return EP_OK;
+}
+
+ep_status_t ep_swiglu(const ep_layout_t* layout, const void* handle_mem, size_t handle_bytes,
+                      const void* gate_up, void* out, hipStream_t stream) {
+  Dims d;
+  HandleView hv;
+  int num_cus = 0;
+  ep_status_t st = payload_common(layout, handle_mem, handle_bytes, &d, &hv);
+  if (st != EP_OK) return st;
+  if (d.cap > 0 && (!gate_up || !out)) return EP_ERR_NULL;
+  if (!aligned16(gate_up) || !aligned16(out)) return EP_ERR_ALIGN;
+  st = current_device(&num_cus);
+  if (st != EP_OK) return st;
+  if (launch_swiglu(d, hv, false, nullptr, gate_up, out, num_cus, stream) != hipSuccess)
+    return EP_ERR_HIP;
+  return EP_OK;
+}
+
+ep_status_t ep_swiglu_bwd(const ep_layout_t* layout, const void* handle_mem,
+                          size_t handle_bytes, const void* grad, const void* gate_up,
+                          void* grad_gate_up, hipStream_t stream) {
+  Dims d;
+  HandleView hv;
+  int num_cus = 0;
+  ep_status_t st = payload_common(layout, handle_mem, handle_bytes, &d, &hv);
+  if (st != EP_OK) return st;
+  if (d.cap > 0 && (!grad || !gate_up || !grad_gate_up)) return EP_ERR_NULL;
+  if (!aligned16(grad) || !aligned16(gate_up) || !aligned16(grad_gate_up)) return EP_ERR_ALIGN;
+  st = current_device(&num_cus);
+  if (st != EP_OK) return st;
+  if (launch_swiglu(d, hv, true, grad, gate_up, grad_gate_up, num_cus, stream) != hipSuccess)
     return EP_ERR_HIP;
   return EP_OK;
 }

@@ -241,5 +241,22 @@ hipError_t launch_reduce_rows(const Dims& d, const HandleView& hv, const void* s
 hipError_t launch_weighted_bwd(const Dims& d, const HandleView& hv, const void* g,
                                const void* y, const float* rw, void* grad_rows, float* grad_w,
                                int num_cus, hipStream_t stream);
+// The experts' products (ep_linear.hip): N output features, d.H input
+// features. The backward skips an output whose pointer is null.
+hipError_t launch_grouped_linear(const Dims& d, const HandleView& hv, const void* x,
+                                 const void* weight, void* out, int64_t N, int num_cus,
+                                 hipStream_t stream);
+hipError_t launch_grouped_linear_bwd(const Dims& d, const HandleView& hv, const void* grad,
+                                     const void* x, const void* weight, void* grad_x,
+                                     void* grad_weight, int64_t N, int num_cus,
+                                     hipStream_t stream);
+// The product with 4-bit weights (ep_quant.hip).
+hipError_t launch_grouped_quant(const Dims& d, const HandleView& hv, const void* x,
+                                const uint8_t* q, const void* scales, const uint8_t* zeros,
+                                void* out, int64_t N, int32_t group, int num_cus,
+                                hipStream_t stream);
+// The gated activation (ep_swiglu.hip); with backward set, its gradient.
+hipError_t launch_swiglu(const Dims& d, const HandleView& hv, bool backward, const void* grad,
+                         const void* gate_up, void* out, int num_cus, hipStream_t stream);
 
 }  // namespace epmi

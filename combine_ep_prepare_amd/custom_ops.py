@@ -11,7 +11,9 @@ name; nothing is computed here.
 
 A layout travels as a list of ints ``[T, K, E, A, H, recv_capacity, dtype,
 flags]`` (``layout_list``); the handle is the uint8 device tensor that
-``prepare`` fills (declared mutated by prepare, read by the others).
+``prepare`` fills (declared mutated by prepare, read by the others). The
+experts' ops take the routing's layout and use the row length of the tensor
+that they are given in place of its H.
 """
 from __future__ import annotations
 
@@ -24,7 +26,10 @@ from . import (DTYPE_BF16, LAYOUT_NO_PAD_FILL, LAYOUT_ZERO_TAIL, TORCH_DTYPE, La
                combine as _combine,
                combine_bwd as _combine_bwd, combine_weighted as _combine_weighted,
                combine_weighted_bwd as _combine_weighted_bwd, dispatch as _dispatch,
-               dispatch_bwd as _dispatch_bwd, prepare as _prepare)
+               dispatch_bwd as _dispatch_bwd, grouped_linear as _grouped_linear,
+               grouped_linear_bwd as _grouped_linear_bwd,
+               grouped_linear_quant as _grouped_linear_quant, prepare as _prepare,
+               swiglu as _swiglu, swiglu_bwd as _swiglu_bwd)
 
 NS = "ep_mi355x"
 
@@ -226,3 +231,110 @@ def _cw_backward(ctx, g):
 
 
 combine_weighted.register_autograd(_cw_backward, setup_context=_cw_setup)
+
+
+# --------------------------------------------------------------------------
+# the experts' products and activation
+# --------------------------------------------------------------------------
+
+def _rows_layout(ll: Sequence[int], hidden: int) -> Layout:
+    return _layout([*ll[:4], hidden, *ll[5:]], zero_tail=True)
+
+
+@torch.library.custom_op(f"{NS}::grouped_linear", mutates_args=())
+def grouped_linear(x: Tensor, weight: Tensor, handle: Tensor, layout: List[int]) -> Tensor:
+    """Each live row of x [cap,H] through its expert's weight [E,N,H]: [cap,N]."""
+    out = torch.empty(x.shape[0], weight.shape[1], dtype=x.dtype, device=x.device)
+    _grouped_linear(_rows_layout(layout, x.shape[1]), handle, x, weight, out)
+    return out
+
+
+@grouped_linear.register_fake
+def _(x, weight, handle, layout):
+    return x.new_empty((x.shape[0], weight.shape[1]))
+
+
+@torch.library.custom_op(f"{NS}::grouped_linear_bwd", mutates_args=())
+def grouped_linear_bwd(grad: Tensor, x: Tensor, weight: Tensor, handle: Tensor,
+                       layout: List[int]) -> Tuple[Tensor, Tensor]:
+    """(grad_x [cap,H], grad_weight [E,N,H])."""
+    gx = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+    gw = torch.empty(weight.shape, dtype=weight.dtype, device=weight.device)
+    _grouped_linear_bwd(_rows_layout(layout, x.shape[1]), handle, grad, x, weight, gx, gw)
+    return gx, gw
+
+
+@grouped_linear_bwd.register_fake
+def _(grad, x, weight, handle, layout):
+    return x.new_empty(x.shape), weight.new_empty(weight.shape)
+
+
+def _linear_setup(ctx, inputs, output):
+    x, weight, handle, layout = inputs
+    ctx.save_for_backward(x, weight, handle)
+    ctx.layout = layout
+
+
+def _linear_backward(ctx, g):
+    x, weight, handle = ctx.saved_tensors
+    gx, gw = grouped_linear_bwd(g.contiguous(), x, weight, handle, ctx.layout)
+    return gx, gw, None, None
+
+
+grouped_linear.register_autograd(_linear_backward, setup_context=_linear_setup)
+
+
+@torch.library.custom_op(f"{NS}::grouped_linear_quant", mutates_args=())
+def grouped_linear_quant(x: Tensor, qweight: Tensor, scales: Tensor, zeros: Optional[Tensor],
+                         handle: Tensor, layout: List[int]) -> Tensor:
+    """``grouped_linear`` with 4-bit weights; no autograd."""
+    out = torch.empty(x.shape[0], scales.shape[1], dtype=x.dtype, device=x.device)
+    _grouped_linear_quant(_rows_layout(layout, x.shape[1]), handle, x, qweight, scales, zeros,
+                          out)
+    return out
+
+
+@grouped_linear_quant.register_fake
+def _(x, qweight, scales, zeros, handle, layout):
+    return x.new_empty((x.shape[0], scales.shape[1]))
+
+
+@torch.library.custom_op(f"{NS}::swiglu", mutates_args=())
+def swiglu(gate_up: Tensor, handle: Tensor, layout: List[int]) -> Tensor:
+    """silu(gate) * up of each live row of gate_up [cap,2I]: [cap,I]."""
+    hidden = gate_up.shape[1] // 2
+    out = torch.empty(gate_up.shape[0], hidden, dtype=gate_up.dtype, device=gate_up.device)
+    _swiglu(_rows_layout(layout, hidden), handle, gate_up, out)
+    return out
+
+
+@swiglu.register_fake
+def _(gate_up, handle, layout):
+    return gate_up.new_empty((gate_up.shape[0], gate_up.shape[1] // 2))
+
+
+@torch.library.custom_op(f"{NS}::swiglu_bwd", mutates_args=())
+def swiglu_bwd(grad: Tensor, gate_up: Tensor, handle: Tensor, layout: List[int]) -> Tensor:
+    """The gradient of gate_up [cap,2I]."""
+    out = torch.empty(gate_up.shape, dtype=gate_up.dtype, device=gate_up.device)
+    _swiglu_bwd(_rows_layout(layout, gate_up.shape[1] // 2), handle, grad, gate_up, out)
+    return out
+
+
+@swiglu_bwd.register_fake
+def _(grad, gate_up, handle, layout):
+    return gate_up.new_empty(gate_up.shape)
+
+
+def _swiglu_setup(ctx, inputs, output):
+    gate_up, handle, layout = inputs
+    ctx.save_for_backward(gate_up, handle)
+    ctx.layout = layout
+
+
+def _swiglu_backward(ctx, g):
+    gate_up, handle = ctx.saved_tensors
+    return swiglu_bwd(g.contiguous(), gate_up, handle, ctx.layout), None, None
+
+
+swiglu.register_autograd(_swiglu_backward, setup_context=_swiglu_setup)

@@ -1,7 +1,9 @@
 /*
  * ep.h -- MoE expert-parallel token routing on one AMD Instinct MI355X
  * (gfx950): prepare, dispatch, combine and their two backward ops, plus a
- * fused weighted combine and its backward.
+ * fused weighted combine and its backward, and the experts' own work between
+ * dispatch and combine: products grouped by expert, with their gradients and
+ * with 4-bit weights, and the gated activation with its gradient.
  *
  * The five per-step calls follow the per-step part of the common C API in
  * "Expert Parallelism: common C API + NCCL EP backend" (section "Per-step
@@ -370,6 +372,101 @@ ep_status_t ep_combine_weighted_bwd(const ep_layout_t* layout, const void* handl
                                     const void* expert_out, const float* recv_topk_weights,
                                     void* grad_expert_out, float* grad_recv_topk_weights,
                                     hipStream_t stream);
+
+/*
+ * The experts' products and activation: what runs between dispatch and
+ * combine, on the segments of a prepared handle. All five are the library's
+ * own addition. They follow the conventions above: only the live rows of a
+ * segment (its valid routes' rows below recv_capacity) are operands, so the
+ * contents of pad rows and of the rows past the live total never matter,
+ * whatever they hold; in an expert-major output the pad rows are zeroed (not
+ * written with EP_LAYOUT_NO_PAD_FILL) and the rows at or past
+ * min(total, recv_capacity) are not written (+0 with EP_LAYOUT_ZERO_TAIL).
+ * The layout's hidden is the row length named at each call; feature counts
+ * (H and N below) are multiples of 8 up to EP_MAX_FEATURES, else
+ * EP_ERR_SHAPE. Sums are held in fp32 and rounded once to the payload type,
+ * in an order that is fixed for given sizes and routing (results are
+ * bit-identical from run to run) and otherwise unspecified. An infinity or
+ * NaN in an operand reaches exactly the outputs whose sums contain it.
+ */
+#define EP_MAX_FEATURES (1 << 20)
+
+/*
+ * Grouped linear: out[r,:] = weight[e] x[r,:] for every live row r of every
+ * expert e, one weight matrix per expert.
+ *   x             payload [recv_capacity,H], H = layout->hidden
+ *   weight        payload [E,N,H]
+ *   out           payload [recv_capacity,N]
+ *   out_features  N
+ */
+ep_status_t ep_grouped_linear(const ep_layout_t* layout, const void* handle_mem,
+                              size_t handle_bytes, const void* x, const void* weight, void* out,
+                              int64_t out_features, hipStream_t stream);
+
+/*
+ * Backward of the grouped linear, with H = layout->hidden (x's row length)
+ * and N = out_features (grad's):
+ *   grad_x[r,:]         = sum over n of grad[r,n] * weight[e,n,:]
+ *   grad_weight[e,n,:]  = sum over the live rows r of e of grad[r,n] * x[r,:]
+ * grad_weight is written whole: an expert without a live row gets +0. Either
+ * output may be NULL and is then skipped, together with the operand only it
+ * needs (weight for grad_x, x for grad_weight); both NULL is EP_ERR_NULL.
+ *   grad         payload [recv_capacity,N]
+ *   x            payload [recv_capacity,H] or NULL
+ *   weight       payload [E,N,H] or NULL
+ *   grad_x       payload [recv_capacity,H] or NULL
+ *   grad_weight  payload [E,N,H] or NULL
+ */
+ep_status_t ep_grouped_linear_bwd(const ep_layout_t* layout, const void* handle_mem,
+                                  size_t handle_bytes, const void* grad, const void* x,
+                                  const void* weight, void* grad_x, void* grad_weight,
+                                  int64_t out_features, hipStream_t stream);
+
+/*
+ * Grouped linear with 4-bit weights, for serving: out[r,:] = W[e] x[r,:] with
+ *   W[e,n,h] = (q[e,n,h] - z[e,n,h/G]) * scales[e,n,h/G],
+ * q in 0..15, G = group_size inputs to a group. Built for few rows per expert
+ * (decoding), right for any number. bf16 and fp16 payloads (fp32 is
+ * EP_ERR_SHAPE); G is 32, 64 or 128 and divides H. The dequantised weight is
+ * never rounded: q is an exact operand, and scale and zero point are applied
+ * to each group's fp32 sum.
+ *   x             payload [recv_capacity,H], H = layout->hidden
+ *   qweight       uint8 [E,N,H/2]; byte h/2 holds input h in its low four
+ *                 bits for even h, in its high four bits for odd h
+ *   scales        payload [E,N,H/G]
+ *   zeros         uint8 [E,N,H/G] (any value is taken as that whole number),
+ *                 or NULL for 8 everywhere
+ *   out           payload [recv_capacity,N]
+ *   out_features  N
+ * qweight, scales and zeros are 16-byte aligned.
+ */
+ep_status_t ep_grouped_linear_quant(const ep_layout_t* layout, const void* handle_mem,
+                                    size_t handle_bytes, const void* x, const uint8_t* qweight,
+                                    const void* scales, const uint8_t* zeros, void* out,
+                                    int64_t out_features, int32_t group_size,
+                                    hipStream_t stream);
+
+/*
+ * Gated activation: out[r,i] = silu(gate_up[r,i]) * gate_up[r,I+i] for every
+ * live row r, silu(g) = g / (1 + exp(-g)), I = layout->hidden.
+ *   gate_up  payload [recv_capacity,2I]
+ *   out      payload [recv_capacity,I]
+ */
+ep_status_t ep_swiglu(const ep_layout_t* layout, const void* handle_mem, size_t handle_bytes,
+                      const void* gate_up, void* out, hipStream_t stream);
+
+/*
+ * Backward of the gated activation: with g, u the halves of a live row and
+ * s = 1 / (1 + exp(-g)),
+ *   grad_gate_up[r,i]   = grad[r,i] * u * s * (1 + g * (1 - s))
+ *   grad_gate_up[r,I+i] = grad[r,i] * g * s
+ *   grad          payload [recv_capacity,I], I = layout->hidden
+ *   gate_up       payload [recv_capacity,2I]
+ *   grad_gate_up  payload [recv_capacity,2I]
+ */
+ep_status_t ep_swiglu_bwd(const ep_layout_t* layout, const void* handle_mem,
+                          size_t handle_bytes, const void* grad, const void* gate_up,
+                          void* grad_gate_up, hipStream_t stream);
 
 /* Copy the handle's status word (EP_STATUS_* bits) to *host_out. Waits for
  * `stream`; not for the hot path. host_out is a host pointer. The library's
