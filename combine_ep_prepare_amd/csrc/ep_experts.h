@@ -1,5 +1,5 @@
 // ep_experts.h -- device helpers of the kernels that work on the expert
-// segments of a receive buffer (ep_linear.hip, ep_quant.hip, ep_swiglu.hip):
+// segments of a receive buffer (ep_linear.hip, ep_decode.hip, ep_swiglu.hip):
 // the live rows of a segment, the list of row tiles over all segments, and
 // the zero rows of an output of any width.
 #pragma once
@@ -87,30 +87,6 @@ __device__ __forceinline__ void write_zero_rows(const HandleHeader& hh, const Ha
   for (int64_t i = first; i < z.n; i += (int64_t)gridDim.x * waves) {
     row16_t* p = static_cast<row16_t*>(out) + zero_row(z, hv.pad_rows, i) * vecs;
     for (int64_t v = lane_id(); v < vecs; v += kWave) store_stream16(p + v, zero);
-  }
-}
-
-// One element of an array of the payload type, widened to fp32, and one fp32
-// value rounded once to it (the conventions of ep.h).
-template <int DT>
-__device__ __forceinline__ float load_elem(const void* p, int64_t i) {
-  if constexpr (DT == EP_DTYPE_BF16) {
-    return __uint_as_float((uint32_t) static_cast<const uint16_t*>(p)[i] << 16);
-  } else if constexpr (DT == EP_DTYPE_FP16) {
-    return f16_to_f32(static_cast<const uint16_t*>(p)[i]);
-  } else {
-    return static_cast<const float*>(p)[i];
-  }
-}
-
-template <int DT>
-__device__ __forceinline__ void store_elem(void* p, int64_t i, float v) {
-  if constexpr (DT == EP_DTYPE_BF16) {
-    static_cast<uint16_t*>(p)[i] = (uint16_t)rne_bf16(v);
-  } else if constexpr (DT == EP_DTYPE_FP16) {
-    static_cast<uint16_t*>(p)[i] = (uint16_t)rne_f16(v);
-  } else {
-    static_cast<uint32_t*>(p)[i] = canon_f32(v);
   }
 }
 

@@ -250,7 +250,10 @@ hipError_t launch_grouped_linear_bwd(const Dims& d, const HandleView& hv, const 
                                      const void* x, const void* weight, void* grad_x,
                                      void* grad_weight, int64_t N, int num_cus,
                                      hipStream_t stream);
-// The product with 4-bit weights (ep_quant.hip).
+// The same product for few rows per expert, 16-bit payloads only, and the
+// product with 4-bit weights (ep_decode.hip).
+hipError_t launch_grouped_few(const Dims& d, const HandleView& hv, const void* x, const void* w,
+                              void* out, int64_t N, int num_cus, hipStream_t stream);
 hipError_t launch_grouped_quant(const Dims& d, const HandleView& hv, const void* x,
                                 const uint8_t* q, const void* scales, const uint8_t* zeros,
                                 void* out, int64_t N, int32_t group, int num_cus,

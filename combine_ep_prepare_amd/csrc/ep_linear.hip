@@ -374,6 +374,7 @@ hipError_t launch_product(const Dims& d, const HandleView& hv, const void* a, co
     const int64_t rows = P == kWeightGrad ? N : d.T * d.K / d.E;
     const int64_t cols = P == kForward ? N : d.H;
     if constexpr (DT != EP_DTYPE_FP32) {
+      if (P == kForward && rows <= 16) return launch_grouped_few(d, hv, a, b, c, N, num_cus, stream);
       if (rows > 128 && cols > 128)
         return launch_tiles<DT, P, 256, 256, 2, 4>(d, hv, a, b, c, N, num_cus, 1, stream);
     }
