@@ -34,8 +34,7 @@ constexpr int kThreads = kWaves * kWave;
 constexpr int kNF = 4;                // 16-column blocks of a wavefront
 constexpr int kCols = 16 * kNF;       // columns of a tile
 constexpr int kRowTile = 16;          // rows of a tile
-constexpr int kStageK = 8192;         // inputs whose scales are staged at once
-constexpr int kRedRow = kCols + 4;    // floats of a row of partial sums in LDS
+constexpr int kLdsRow = kCols + 4;    // floats of a row of kCols in LDS
 
 template <int DT>
 __device__ __forceinline__ f32x4 mma16(row16_t n, row16_t m, f32x4 acc) {
@@ -56,12 +55,12 @@ struct Offset {
 };
 
 // Eight weights of a word as offset values, in the order 0 4 1 5 2 6 3 7.
-template <int DT>
-__device__ __forceinline__ row16_t spread(uint32_t w) {
+// `bits` is Offset::kBits from a vector register: with the mask in a scalar
+// one, each pair is one mask-and-or (two constants cannot both be scalar).
+__device__ __forceinline__ row16_t spread(uint32_t w, uint32_t bits) {
   constexpr uint32_t kMask = 0x000F000Fu;
-  return row16_t{(w & kMask) | Offset<DT>::kBits, ((w >> 4) & kMask) | Offset<DT>::kBits,
-                 ((w >> 8) & kMask) | Offset<DT>::kBits,
-                 ((w >> 12) & kMask) | Offset<DT>::kBits};
+  return row16_t{(w & kMask) | bits, ((w >> 4) & kMask) | bits, ((w >> 8) & kMask) | bits,
+                 ((w >> 12) & kMask) | bits};
 }
 
 // Eight 16-bit values of x put into the same order.
@@ -82,102 +81,135 @@ __device__ __forceinline__ row16_t transpose_quarters(row16_t v) {
   return row16_t{c[0], c[1], e[0], e[1]};
 }
 
-// The inputs of one step of k for a lane. A lane works on column lane % 16 of
-// each block of weights and row lane % 16 of x; its quarter q = lane / 16
-// picks the part of k.
-// 4 bits: a step is 128 inputs, one 16-byte load of 32 weights a lane and
-// block. With G = 128 word t of quarter q is inputs 32 q + 8 t; for smaller
-// groups, whose sums must not mix, the words are transposed over the quarters
-// first and word t of quarter q is inputs 32 t + 8 q.
-// 16 bits: a step is 64 inputs, two loads a lane and block.
-template <bool QUANT>
-struct Step {
-  static constexpr int kStep = QUANT ? 128 : 64;
-  static constexpr int kParts = QUANT ? 4 : 2;   // matrix instructions of a block
-  static constexpr int kWords = QUANT ? 1 : 2;   // 16-byte loads of a block
-  row16_t w[kNF][kWords];
-  row16_t x[kParts];
-};
-
-// Where a lane reads: the tile's weights and rows (the same for the block)
-// and its own column of each block and row, as offsets from there.
-struct Source {
-  const char* w;
-  const char* x;
-  uint32_t w_off[kNF];
-  uint32_t x_off;
-};
-
+// A step of k for a wavefront: 128 bytes of each of the tile's 64 columns, i.e.
+// 256 inputs of 4 bits or 64 of 16 bits, in two halves of 64 bytes.
+//
+// A weight load is 8 columns x 128 bytes: whole lines, each of them asked for
+// once, so that they can bypass the caches' retention (nontemporal). A lane
+// of a matrix instruction wants 16 bytes of column lane % 16 instead; loads
+// of that shape touch 16 lines of 64 bytes and ran at 5.4 TB/s where these
+// run at 6.8 (batch of 32, 256 experts, weights only). So the lines go from
+// registers through a part of LDS that belongs to the wavefront alone, with
+// no barrier: chunk c of column n at slot c ^ (n & 7).
+// While a step is multiplied out of LDS, the next one's loads are in flight.
+//
+// The quarter q = lane / 16 picks the part of k. 4 bits: with G = 128 word t
+// of quarter q is inputs 32 q + 8 t of the half; for smaller groups, whose
+// sums must not mix, the words are transposed over the quarters first and
+// word t of quarter q is inputs 32 t + 8 q. 16 bits: inputs 8 q of the half.
 template <int DT, bool QUANT, int G, bool ZEROS>
-struct Tile {
-  using S = Step<QUANT>;
-  static constexpr int kStep = S::kStep;
-  static constexpr int kGroups = QUANT ? kStep / G : 1;  // groups of a step
+struct Stream {
+  static constexpr int kStep = QUANT ? 256 : 64;
+  static constexpr int kHalf = kStep / 2;
+  static constexpr int kParts = QUANT ? 4 : 1;           // matrix instructions of a half
+  static constexpr int kGroups = QUANT ? kHalf / G : 1;  // groups of a half
   static constexpr int kPer = 4 / kGroups;               // 4 bits: parts of a group
+  static constexpr int kRows = QUANT ? 2 * kGroups : 0;  // groups of a step
+  static constexpr int kLoads = kCols / 8;
+  // LDS of a wavefront: the weights of a step (in the end its sums), then
+  // the step's scales and zero points as [group][column]
+  static constexpr int kLds = kCols * 128 + (ZEROS ? 2 : 1) * kRows * kLdsRow * 4;
 
-  // Loads the step that starts at input k0. Past the end of the row it reads
-  // the row's start instead; finish() takes those values out.
-  __device__ static __forceinline__ void load(S& s, const Source& src, int32_t k0, int32_t H) {
+  // Where a tile's operands start (the same for the whole block), and a
+  // lane's row of x.
+  struct Source {
+    const char* w;
+    const char* x;
+    const uint16_t* scales;
+    const uint8_t* zeros;
+    uint32_t x_off;
+    int32_t cols;
+  };
+
+  row16_t w[kLoads];
+  row16_t x[2][kParts];
+  uint16_t scale[QUANT ? kRows : 1];   // of column `lane`
+  uint8_t zero[QUANT ? kRows : 1];
+
+  __device__ static __forceinline__ int32_t input(int half, int t) {
     const int q = lane_id() >> 4;
+    return half * kHalf + (QUANT && G == 128 ? 32 * q + 8 * t : 32 * t + 8 * q);
+  }
+
+  // Loads of the step that starts at input k0. One that passes the end of the
+  // row (PART) reads the row's start in place of what is not there and takes
+  // it out again: x counts zero, and so do 16-bit weights and scales.
+  template <bool PART>
+  __device__ __forceinline__ void load_weights(const Source& s, int32_t k0, int32_t H) {
+    const int lane = lane_id();
+    const uint32_t w_row = QUANT ? H / 2 : H * 2;
+    const int chunk = (lane & 7) ^ (lane >> 3);
+    const bool in = !PART || k0 + chunk * (kStep / 8) < H;
+    const uint32_t at = (uint32_t)(lane >> 3) * w_row + chunk * 16;
+    const char* from = s.w + (QUANT ? k0 / 2 : k0 * 2);
+    static_for<kLoads>([&](auto j) {
+      const char* column = from + (j * 8 < s.cols ? j * 8 * (int64_t)w_row : 0);
+      if constexpr (PART) column -= in ? 0 : (QUANT ? k0 / 2 : k0 * 2) + chunk * 16;
+      w[j] = __builtin_nontemporal_load(reinterpret_cast<const row16_t*>(column + at));
+      if constexpr (PART && !QUANT) w[j] = in ? w[j] : row16_t{0, 0, 0, 0};
+    });
     if constexpr (QUANT) {
-      const int32_t k = k0 + 32 * q;
-      const uint32_t at = (k < H ? k : 0) / 2;
-      static_for<kNF>([&](auto j) {
-        s.w[j][0] = __builtin_nontemporal_load(
-            reinterpret_cast<const row16_t*>(src.w + (src.w_off[j] + at)));
-      });
-    } else {
-      static_for<S::kWords>([&](auto t) {
-        const int32_t k = k0 + 32 * t + 8 * q;
-        const uint32_t at = (k < H ? k : 0) * 2;
-        static_for<kNF>([&](auto j) {
-          s.w[j][t] = __builtin_nontemporal_load(
-              reinterpret_cast<const row16_t*>(src.w + (src.w_off[j] + at)));
+      const int32_t all = H / G, g0 = k0 / G;
+      const int64_t row = (int64_t)(lane < s.cols ? lane : 0) * all + g0;
+      if constexpr (PART) {
+        static_for<kRows>([&](auto g) {
+          const bool have = g0 + g < all;
+          scale[g] = have ? s.scales[row + g] : 0;
+          if constexpr (ZEROS) zero[g] = have ? s.zeros[row + g] : 0;
         });
+      } else {
+        __builtin_memcpy(scale, s.scales + row, sizeof(scale));
+        if constexpr (ZEROS) __builtin_memcpy(zero, s.zeros + row, sizeof(zero));
+      }
+    }
+  }
+  template <bool PART>
+  __device__ __forceinline__ void load_x(const Source& s, int half, int32_t k0, int32_t H) {
+    static_for<kParts>([&](auto t) {
+      const int32_t k = k0 + input(half, t);
+      const bool in = !PART || k < H;
+      const row16_t v =
+          *reinterpret_cast<const row16_t*>(s.x + (s.x_off + (uint32_t)(in ? k : 0) * 2));
+      x[half][t] = in ? v : row16_t{0, 0, 0, 0};
+    });
+  }
+
+  // The loaded weights and scales into the wavefront's LDS. Its lanes write
+  // and read it in program order; the fences keep the compiler to it.
+  __device__ __forceinline__ void put(char* lds) const {
+    const int lane = lane_id();
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    static_for<kLoads>([&](auto j) {
+      *reinterpret_cast<row16_t*>(lds + j * 1024 + lane * 16) = w[j];
+    });
+    if constexpr (QUANT) {
+      float* scales = reinterpret_cast<float*>(lds + kCols * 128);
+      float* zeros = scales + kRows * kLdsRow;
+      static_for<kRows>([&](auto g) {
+        scales[g * kLdsRow + lane] = DT == EP_DTYPE_BF16
+                                         ? __uint_as_float((uint32_t)scale[g] << 16)
+                                         : f16_to_f32(scale[g]);
+        if constexpr (ZEROS) zeros[g * kLdsRow + lane] = Offset<DT>::kValue + (float)zero[g];
       });
     }
-    static_for<S::kParts>([&](auto t) {
-      const int32_t k = input(k0, t);
-      const uint32_t at = (k < H ? k : 0) * 2;
-      s.x[t] = *reinterpret_cast<const row16_t*>(src.x + (src.x_off + at));
-    });
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
   }
 
-  // The input that part t of a step starts at, for this lane.
-  __device__ static __forceinline__ int32_t input(int32_t k0, int t) {
-    const int q = lane_id() >> 4;
-    return k0 + (QUANT && G == 128 ? 32 * q + 8 * t : 32 * t + 8 * q);
-  }
-
-  // Inputs past the end of the row count nothing: x is zero there, and so
-  // are 16-bit weights.
-  __device__ static __forceinline__ void finish(S& s, int32_t k0, int32_t H) {
-    if (k0 + kStep <= H) return;
-    const row16_t zero = {0, 0, 0, 0};
-    static_for<S::kParts>([&](auto t) {
-      const bool in = input(k0, t) < H;
-      s.x[t] = in ? s.x[t] : zero;
-      if constexpr (!QUANT) {
-        static_for<kNF>([&](auto j) { s.w[j][t] = in ? s.w[j][t] : zero; });
-      }
-    });
-  }
-
-  // scales, zeros: the step's first group in LDS, [group][column].
-  __device__ static __forceinline__ void multiply(S& s, int32_t k0, int32_t H,
-                                                  const uint16_t* scales, const uint8_t* zeros,
+  // One half out of LDS; xs is its x, already interleaved for 4 bits.
+  __device__ static __forceinline__ void multiply(const char* lds, int half,
+                                                  const row16_t (&xs)[kParts], uint32_t bits,
                                                   f32x4 (&acc)[kNF]) {
-    finish(s, k0, H);
+    const int lane = lane_id(), q = lane >> 4, i16 = lane & 15;
+    const char* mine = lds + i16 * 128 + (((half * 4 + q) ^ (i16 & 7)) << 4);
     if constexpr (!QUANT) {
-      static_for<S::kParts>([&](auto t) {
-        static_for<kNF>([&](auto j) { acc[j] = mma16<DT>(s.w[j][t], s.x[t], acc[j]); });
+      static_for<kNF>([&](auto j) {
+        acc[j] = mma16<DT>(*reinterpret_cast<const row16_t*>(mine + j * 2048), xs[0], acc[j]);
       });
     } else {
-      const int q = lane_id() >> 4;
-      row16_t xs[4];
+      const float* scales = reinterpret_cast<const float*>(lds + kCols * 128);
+      const float* zeros = scales + kRows * kLdsRow;
       f32x4 sum[kGroups];
       constexpr uint32_t one = Offset<DT>::kOnes;
-      static_for<4>([&](auto t) { xs[t] = interleave(s.x[t]); });
       static_for<kGroups>([&](auto g) {
         sum[g] = f32x4{0.f, 0.f, 0.f, 0.f};
         static_for<kPer>([&](auto u) {
@@ -185,32 +217,21 @@ struct Tile {
         });
       });
       static_for<kNF>([&](auto j) {
-        const row16_t words = G == 128 ? s.w[j][0] : transpose_quarters(s.w[j][0]);
+        row16_t words = *reinterpret_cast<const row16_t*>(mine + j * 2048);
+        if constexpr (G < 128) words = transpose_quarters(words);
         static_for<kGroups>([&](auto g) {
           // one group's operands at a time: read ahead for all blocks, the
           // scales alone would take more registers than a wavefront has
           __builtin_amdgcn_sched_barrier(0);
-          const int at = g * kCols + j * 16 + q * 4;
-          const u32x2 sc = *reinterpret_cast<const u32x2*>(scales + at);
-          f32x4 scale, zero;
-          if constexpr (DT == EP_DTYPE_BF16) {
-            scale = f32x4{bf16_lo(sc[0]), bf16_hi(sc[0]), bf16_lo(sc[1]), bf16_hi(sc[1])};
-          } else {
-            scale = f32x4{f16_to_f32(sc[0] & 0xFFFFu), f16_to_f32(sc[0] >> 16),
-                          f16_to_f32(sc[1] & 0xFFFFu), f16_to_f32(sc[1] >> 16)};
-          }
-          if constexpr (ZEROS) {
-            const uint32_t z = *reinterpret_cast<const uint32_t*>(zeros + at);
-            static_for<4>([&](auto c) {
-              zero[c.value] = Offset<DT>::kValue + (float)((z >> (8 * c.value)) & 255u);
-            });
-          } else {
-            static_for<4>([&](auto c) { zero[c.value] = Offset<DT>::kValue + 8.f; });
-          }
+          const int at = (half * kGroups + g) * kLdsRow + j * 16 + q * 4;
+          const f32x4 scale = *reinterpret_cast<const f32x4*>(scales + at);
+          constexpr float z8 = Offset<DT>::kValue + 8.f;
+          f32x4 zero = {z8, z8, z8, z8};
+          if constexpr (ZEROS) zero = *reinterpret_cast<const f32x4*>(zeros + at);
           f32x4 part = {0.f, 0.f, 0.f, 0.f};
           static_for<kPer>([&](auto u) {
             constexpr int t = g.value * kPer + u.value;
-            part = mma16<DT>(spread<DT>(words[t]), xs[t], part);
+            part = mma16<DT>(spread(words[t], bits), xs[t], part);
           });
           static_for<4>([&](auto c) {
             const float v = __builtin_fmaf(-zero[c.value], sum[g][0], part[c.value]);
@@ -220,120 +241,37 @@ struct Tile {
       });
     }
   }
+
+  // Multiplies the loaded step; the next one's loads (step k1 of `next`) are
+  // issued as the registers they fill are done with.
+  template <bool MORE>
+  __device__ __forceinline__ void step(char* lds, const Source& next, int32_t k1, int32_t H,
+                                       uint32_t bits, f32x4 (&acc)[kNF]) {
+    put(lds);
+    if constexpr (MORE) load_weights<false>(next, k1, H);
+    static_for<2>([&](auto half) {
+      row16_t xs[kParts];
+      static_for<kParts>([&](auto t) {
+        xs[t] = QUANT ? interleave(x[half][t]) : x[half][t];
+      });
+      if constexpr (MORE) load_x<false>(next, half, k1, H);
+      multiply(lds, half, xs, bits, acc);
+    });
+  }
 };
 
-// Blocks (of one wavefront a SIMD) that the registers allow: small groups
-// keep a few more values in flight.
-constexpr int blocks_per_cu(bool quant, int group) { return quant && group < 128 ? 3 : 4; }
-
-struct Lds {
-  uint16_t* scales;
-  uint8_t* zeros;
-  float* sums;
-};
-
-// One tile: up to 16 rows of expert e by kCols columns. The wavefronts take
-// consecutive parts of the steps of k and add their sums in LDS.
+// Up to 16 rows of an expert by kCols columns a block step. The wavefronts
+// take the steps of k in turn, so that the block reads 512 bytes of a column
+// side by side, and add their sums in LDS at the end; by then each has the
+// first loads of the block's next tile in flight.
 template <int DT, bool QUANT, int G, bool ZEROS>
-__device__ __forceinline__ void run_tile(const Lds& lds, int32_t H, int64_t N, int e,
-                                         int64_t row0, int32_t rows, int64_t n0, const char* x,
-                                         const char* w, const uint16_t* scales,
-                                         const uint8_t* zeros, void* out) {
-  using T = Tile<DT, QUANT, G, ZEROS>;
-  constexpr int kStep = T::kStep;
-  const int lane = lane_id(), i16 = lane & 15;
-  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
-  const uint32_t w_row = QUANT ? H / 2 : H * 2;
-  const int32_t cols = (int32_t)(N - n0 < kCols ? N - n0 : kCols);
-  Source src;
-  src.w = w + ((int64_t)e * N + n0) * w_row;
-  src.x = x + row0 * H * 2;
-  static_for<kNF>([&](auto j) {
-    const int32_t n = j * 16 + i16;
-    src.w_off[j] = (uint32_t)(n < cols ? n : cols - 1) * w_row;
-  });
-  src.x_off = (uint32_t)(i16 < rows ? i16 : rows - 1) * (uint32_t)(H * 2);
-  f32x4 acc[kNF];
-  static_for<kNF>([&](auto j) { acc[j] = f32x4{0.f, 0.f, 0.f, 0.f}; });
-  for (int32_t c0 = 0; c0 < H; c0 += QUANT ? kStageK : H) {
-    const int32_t left = H - c0;
-    const int32_t span = QUANT && left > kStageK ? kStageK : left;
-    const int32_t steps = (span + kStep - 1) / kStep;
-    const int32_t per = (steps + kWaves - 1) / kWaves;
-    int32_t s0 = wave * per;
-    const int32_t s1 = s0 + per < steps ? s0 + per : steps;
-    typename T::S a, b;
-    if (s0 < s1) T::load(a, src, c0 + s0 * kStep, H);
-    if constexpr (QUANT) {
-      // the scales of the span, transposed to [group][column]; groups past
-      // the end of the row and columns past N are zeros
-      const int32_t groups = steps * T::kGroups;
-      const int64_t all = H / G, g0 = c0 / G;
-      __syncthreads();
-      for (int32_t t = threadIdx.x; t < groups * kCols; t += kThreads) {
-        const int32_t n = t / groups, g = t - n * groups;
-        const bool in = n < cols && g0 + g < all;
-        const int64_t at = ((int64_t)e * N + n0 + n) * all + g0 + g;
-        lds.scales[g * kCols + n] = in ? scales[at] : 0;
-        if constexpr (ZEROS) lds.zeros[g * kCols + n] = in ? zeros[at] : 0;
-      }
-      __syncthreads();
-    }
-    auto load = [&](typename T::S& to, int32_t s) {
-      T::load(to, src, c0 + (s < s1 ? s : s1 - 1) * kStep, H);
-    };
-    auto multiply = [&](typename T::S& from, int32_t s) {
-      const int32_t at = s * T::kGroups * kCols;
-      T::multiply(from, c0 + s * kStep, H, lds.scales + at, lds.zeros + at, acc);
-    };
-    // two steps in turn, each loaded while the other is multiplied
-    for (; s0 < s1; s0 += 2) {
-      load(b, s0 + 1);
-      multiply(a, s0);
-      load(a, s0 + 2);
-      if (s0 + 1 < s1) multiply(b, s0 + 1);
-    }
-  }
-  static_for<kNF>([&](auto j) {
-    float* p = lds.sums + (wave * 16 + i16) * kRedRow + j * 16 + (lane >> 4) * 4;
-    *reinterpret_cast<f32x4*>(p) = acc[j];
-  });
-  __syncthreads();
-  // 16 rows x 64 columns by 256 threads: four columns of a row each
-  const int m = threadIdx.x / 16, n = threadIdx.x % 16 * 4;
-  f32x4 sum = *reinterpret_cast<const f32x4*>(lds.sums + m * kRedRow + n);
-  static_for<kWaves - 1>([&](auto v) {
-    sum += *reinterpret_cast<const f32x4*>(lds.sums + ((v + 1) * 16 + m) * kRedRow + n);
-  });
-  if (m < rows && n < cols) {
-    u32x2 o;
-    if constexpr (DT == EP_DTYPE_BF16) {
-      o = u32x2{rne_bf16(sum[0]) | (rne_bf16(sum[1]) << 16),
-                rne_bf16(sum[2]) | (rne_bf16(sum[3]) << 16)};
-    } else {
-      o = u32x2{rne_f16(sum[0]) | (rne_f16(sum[1]) << 16),
-                rne_f16(sum[2]) | (rne_f16(sum[3]) << 16)};
-    }
-    *reinterpret_cast<u32x2*>(static_cast<uint16_t*>(out) + (row0 + m) * N + n0 + n) = o;
-  }
-  __syncthreads();  // the sums are read before the next tile writes its own
-}
-
-template <int DT, bool QUANT, int G, bool ZEROS>
-__global__ void __launch_bounds__(kThreads, blocks_per_cu(QUANT, G))
-    few_rows_kernel(Dims d, HandleView hv, const void* __restrict__ x,
-                    const void* __restrict__ w, const uint16_t* __restrict__ scales,
-                    const uint8_t* __restrict__ zeros, void* __restrict__ out, int64_t N,
-                    int32_t scale_bytes) {
+__global__ void __launch_bounds__(kThreads, 3)
+    few_rows_kernel(Dims d, HandleView hv, const char* __restrict__ x,
+                    const char* __restrict__ w, const uint16_t* __restrict__ scales,
+                    const uint8_t* __restrict__ zeros, uint16_t* __restrict__ out, int64_t N) {
+  using S = Stream<DT, QUANT, G, ZEROS>;
   extern __shared__ __align__(16) char mem[];
-  Lds lds;
-  lds.sums = reinterpret_cast<float*>(mem);
-  char* p = mem + kWaves * 16 * kRedRow * sizeof(float);
-  lds.scales = reinterpret_cast<uint16_t*>(p);
-  p += scale_bytes;
-  lds.zeros = reinterpret_cast<uint8_t*>(p);
-  if (ZEROS) p += scale_bytes / 2;
-  int32_t* tile_start = reinterpret_cast<int32_t*>(p);
+  int32_t* tile_start = reinterpret_cast<int32_t*>(mem + kWaves * S::kLds);
   const HandleHeader hh = *hv.header;
   if (!handle_matches(hh, d)) {
     if (blockIdx.x == 0 && threadIdx.x == 0) atomicOr(&hv.header->status, EP_STATUS_LAYOUT);
@@ -341,8 +279,20 @@ __global__ void __launch_bounds__(kThreads, blocks_per_cu(QUANT, G))
   }
   const int64_t row_tiles =
       list_tiles<kThreads>(hv, d, kRowTile, tile_start, tile_start + d.E + 1);
-  const int64_t ct = (N + kCols - 1) / kCols;
-  for (int64_t t = blockIdx.x; t < row_tiles * ct; t += gridDim.x) {
+  const int64_t ct = (N + kCols - 1) / kCols, tiles = row_tiles * ct;
+  const int32_t H = (int32_t)d.H;
+  const int lane = lane_id(), i16 = lane & 15;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+  char* lds = mem + wave * S::kLds;
+  uint32_t bits = Offset<DT>::kBits;
+  asm("" : "+v"(bits));
+
+  struct Place {
+    typename S::Source src;
+    int64_t out;   // first row and column of the tile in `out`
+    int32_t rows;
+  };
+  auto place = [&](int64_t t) {
     // the row tiles of an expert are neighbours: they share their weights
     const int e = __builtin_amdgcn_readfirstlane(
         expert_of_tile(tile_start, d.E, (int32_t)(t / ct)));
@@ -352,10 +302,78 @@ __global__ void __launch_bounds__(kThreads, blocks_per_cu(QUANT, G))
     const int32_t m0 =
         __builtin_amdgcn_readfirstlane((int32_t)(in_e - (int64_t)ni * rts)) * kRowTile;
     const Segment s = segment_of(hv, d, e);
-    run_tile<DT, QUANT, G, ZEROS>(lds, (int32_t)d.H, N, e, s.row + m0,
-                                  s.rows - m0 < kRowTile ? s.rows - m0 : kRowTile,
-                                  (int64_t)ni * kCols, static_cast<const char*>(x),
-                                  static_cast<const char*>(w), scales, zeros, out);
+    const int64_t n0 = (int64_t)ni * kCols, column = (int64_t)e * N + n0;
+    Place p;
+    p.rows = s.rows - m0 < kRowTile ? s.rows - m0 : kRowTile;
+    p.out = (s.row + m0) * N + n0;
+    p.src.w = w + column * (QUANT ? H / 2 : H * 2);
+    p.src.x = x + (s.row + m0) * H * 2;
+    p.src.scales = QUANT ? scales + column * (H / G) : nullptr;
+    p.src.zeros = ZEROS ? zeros + column * (H / G) : nullptr;
+    p.src.x_off = (uint32_t)(i16 < p.rows ? i16 : p.rows - 1) * (uint32_t)(H * 2);
+    p.src.cols = (int32_t)(N - n0 < kCols ? N - n0 : kCols);
+    return p;
+  };
+  const int32_t full = H / S::kStep;                      // whole steps
+  const int32_t first = wave * S::kStep, stride = kWaves * S::kStep;
+  S s;
+  auto load = [&](const Place& p) {
+    if (wave < full) {
+      s.template load_weights<false>(p.src, first, H);
+      s.template load_x<false>(p.src, 0, first, H);
+      s.template load_x<false>(p.src, 1, first, H);
+    }
+  };
+  Place next;
+  if ((int64_t)blockIdx.x < tiles) {
+    next = place(blockIdx.x);
+    load(next);
+  }
+  for (int64_t t = blockIdx.x; t < tiles; t += gridDim.x) {
+    const Place cur = next;
+    f32x4 acc[kNF];
+    static_for<kNF>([&](auto j) { acc[j] = f32x4{0.f, 0.f, 0.f, 0.f}; });
+    if (wave < full) {
+      int32_t k = first;
+      for (; k + stride < full * S::kStep; k += stride)
+        s.template step<true>(lds, cur.src, k + stride, H, bits, acc);
+      s.template step<false>(lds, cur.src, 0, H, bits, acc);
+    }
+    if (full * S::kStep < H && wave == kWaves - 1) {
+      s.template load_weights<true>(cur.src, full * S::kStep, H);
+      s.template load_x<true>(cur.src, 0, full * S::kStep, H);
+      s.template load_x<true>(cur.src, 1, full * S::kStep, H);
+      s.template step<false>(lds, cur.src, 0, H, bits, acc);
+    }
+    if (t + gridDim.x < tiles) {
+      next = place(t + gridDim.x);
+      load(next);
+    }
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    static_for<kNF>([&](auto j) {
+      float* p = reinterpret_cast<float*>(lds) + i16 * kLdsRow + j * 16 + (lane >> 4) * 4;
+      *reinterpret_cast<f32x4*>(p) = acc[j];
+    });
+    __syncthreads();
+    // four columns of a row a thread
+    const int m = threadIdx.x / (kCols / 4), n = threadIdx.x % (kCols / 4) * 4;
+    if (m < cur.rows && n < cur.src.cols) {
+      const char* p = mem + (m * kLdsRow + n) * 4;
+      f32x4 sum = *reinterpret_cast<const f32x4*>(p);
+      static_for<kWaves - 1>([&](auto v) {
+        sum += *reinterpret_cast<const f32x4*>(p + (v + 1) * S::kLds);
+      });
+      u32x2 o;
+      if constexpr (DT == EP_DTYPE_BF16) {
+        o = u32x2{rne_bf16(sum[0]) | (rne_bf16(sum[1]) << 16),
+                  rne_bf16(sum[2]) | (rne_bf16(sum[3]) << 16)};
+      } else {
+        o = u32x2{rne_f16(sum[0]) | (rne_f16(sum[1]) << 16),
+                  rne_f16(sum[2]) | (rne_f16(sum[3]) << 16)};
+      }
+      *reinterpret_cast<u32x2*>(out + cur.out + m * N + n) = o;
+    }
+    __syncthreads();  // the sums are read before the next tile's weights
   }
   write_zero_rows(hh, hv, d, out, N * 2 / 16);
 }
@@ -367,19 +385,14 @@ hipError_t launch_few_rows(const Dims& d, const HandleView& hv, const void* x, c
   const int64_t ct = (N + kCols - 1) / kCols;
   const int64_t routes = d.T * d.K < d.cap ? d.T * d.K : d.cap;
   int64_t blocks = (routes / kRowTile + (d.E < routes ? d.E : routes)) * ct;
-  const int64_t most = (int64_t)num_cus * blocks_per_cu(QUANT, G);
+  const int64_t most = (int64_t)num_cus * 3;
   if (blocks > most) blocks = most;
   if (blocks < 1) blocks = 1;
-  size_t scale_bytes = 0;
-  if (QUANT) {
-    const int64_t span = d.H < kStageK ? d.H : kStageK;
-    scale_bytes = (size_t)((span + 127) / 128 * 128 / G) * kCols * 2;
-  }
-  const size_t lds = kWaves * 16 * kRedRow * sizeof(float) +
-                     (ZEROS ? scale_bytes + scale_bytes / 2 : scale_bytes) +
+  const size_t lds = kWaves * (size_t)Stream<DT, QUANT, G, ZEROS>::kLds +
                      sizeof(int32_t) * (size_t)(d.E + 1 + kWaves);
   few_rows_kernel<DT, QUANT, G, ZEROS><<<dim3((uint32_t)blocks), dim3(kThreads), lds, stream>>>(
-      d, hv, x, w, static_cast<const uint16_t*>(scales), zeros, out, N, (int32_t)scale_bytes);
+      d, hv, static_cast<const char*>(x), static_cast<const char*>(w),
+      static_cast<const uint16_t*>(scales), zeros, static_cast<uint16_t*>(out), N);
   return hipGetLastError();
 }
 
