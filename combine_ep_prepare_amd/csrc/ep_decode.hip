@@ -260,12 +260,18 @@ struct Stream {
   }
 };
 
+// Blocks (of one wavefront a SIMD) to a CU: as many as the registers hold. The
+// 4-bit form in the 128 registers that four leave spills, at twice the time;
+// 16-bit weights with four against three ran 90 against 95 us (sixteen
+// tokens, top-8 of 128).
+constexpr int blocks_per_cu(bool quant) { return quant ? 3 : 4; }
+
 // Up to 16 rows of an expert by kCols columns a block step. The wavefronts
 // take the steps of k in turn, so that the block reads 512 bytes of a column
 // side by side, and add their sums in LDS at the end; by then each has the
 // first loads of the block's next tile in flight.
 template <int DT, bool QUANT, int G, bool ZEROS>
-__global__ void __launch_bounds__(kThreads, 3)
+__global__ void __launch_bounds__(kThreads, blocks_per_cu(QUANT))
     few_rows_kernel(Dims d, HandleView hv, const char* __restrict__ x,
                     const char* __restrict__ w, const uint16_t* __restrict__ scales,
                     const uint8_t* __restrict__ zeros, uint16_t* __restrict__ out, int64_t N) {
@@ -385,7 +391,7 @@ hipError_t launch_few_rows(const Dims& d, const HandleView& hv, const void* x, c
   const int64_t ct = (N + kCols - 1) / kCols;
   const int64_t routes = d.T * d.K < d.cap ? d.T * d.K : d.cap;
   int64_t blocks = (routes / kRowTile + (d.E < routes ? d.E : routes)) * ct;
-  const int64_t most = (int64_t)num_cus * 3;
+  const int64_t most = (int64_t)num_cus * blocks_per_cu(QUANT);
   if (blocks > most) blocks = most;
   if (blocks < 1) blocks = 1;
   const size_t lds = kWaves * (size_t)Stream<DT, QUANT, G, ZEROS>::kLds +

@@ -172,6 +172,8 @@ __device__ __forceinline__ void store4(void* p, int64_t i, f32x4 v) {
 // Row tiles of an expert whose column tiles run together: with the columns
 // dealt after them, the tiles in flight on an XCD share both operands.
 constexpr int kGroup = 8;
+// Weight-gradient tiles that go to one XCD together: one for each of its CUs.
+constexpr int kChunk = 32;
 
 
 // One block step is a BM x BN tile of C: WM x WN wavefronts, each with a part
@@ -212,11 +214,13 @@ __global__ void __launch_bounds__(WM* WN* kWave)
   const int wm = wave / WN, wn = wave % WN;
   const int lane = lane_id();
   const uint32_t lds_base = (uint32_t)(uintptr_t)(lds_char*)lds;
-  // Blocks are dealt round-robin to the XCDs: the tiles of a round that one
-  // XCD works on are consecutive.
-  const int64_t grid = gridDim.x, xcds = grid % kRunXcds == 0 ? kRunXcds : 1;
-  const int64_t slots = grid / xcds;
-  for (int64_t t = (blockIdx.x % xcds) * slots + blockIdx.x / xcds; t < tiles; t += grid) {
+  // Blocks are dealt round-robin to the XCDs: chunks of consecutive tiles go
+  // to one XCD each in turn. A grid of fewer blocks than tiles (not wgrad)
+  // makes a chunk of what an XCD works on at once.
+  const int64_t slots = P == kWeightGrad ? kChunk : gridDim.x / kRunXcds;
+  const int64_t xcd = blockIdx.x % kRunXcds, slot = blockIdx.x / kRunXcds;
+  int64_t t = ((slot / slots) * kRunXcds + xcd) * slots + slot % slots;
+  for (; t < tiles; t += P == kWeightGrad ? tiles : (int64_t)gridDim.x) {
     // tile t: expert e, row tile mi, column tile ni
     int e;
     int64_t first;
@@ -358,9 +362,10 @@ hipError_t launch_tiles(const Dims& d, const HandleView& hv, const void* a, cons
     const int64_t most = (int64_t)num_cus * per_cu;
     if (blocks > most) blocks = most;
   }
-  blocks = (blocks + kRunXcds - 1) / kRunXcds * kRunXcds;
-  if (blocks < kRunXcds) blocks = kRunXcds;
-  if (blocks > 0x7FFFFFF8) blocks = 0x7FFFFFF8;
+  const int64_t unit = P == kWeightGrad ? kRunXcds * kChunk : kRunXcds;
+  blocks = (blocks + unit - 1) / unit * unit;
+  if (blocks < unit) blocks = unit;
+  if (blocks > 0x7FFFFF00) return hipErrorInvalidConfiguration;
   const size_t lds = 2 * (size_t)(BM + BN) * 128 + sizeof(int32_t) * (size_t)(d.E + 1 + 16);
   kernel<<<dim3((uint32_t)blocks), dim3(WM * WN * kWave), lds, stream>>>(d, hv, a, b, c, N);
   return hipGetLastError();
