@@ -50,17 +50,28 @@ __device__ __forceinline__ void mma(f32x4& acc, row16_t n, row16_t m) {
 // past them reads zeros.
 __device__ __forceinline__ row16_t buffer_of(const void* p, uint32_t bytes) {
   const uint64_t a = reinterpret_cast<uint64_t>(p);
-  return row16_t{(uint32_t)a, (uint32_t)(a >> 32) & 0xFFFFu, bytes, 0x00020000u};
+  // the same in every lane; the load wants it in scalar registers
+  return row16_t{(uint32_t)__builtin_amdgcn_readfirstlane((int)a),
+                 (uint32_t)__builtin_amdgcn_readfirstlane((int)(a >> 32)) & 0xFFFFu,
+                 (uint32_t)__builtin_amdgcn_readfirstlane((int)bytes), 0x00020000u};
 }
 
 // An offset past every buffer of a tile (256 rows of EP_MAX_FEATURES values).
 constexpr uint32_t kOutside = 0x40000000u;
 
 // 16 bytes per lane from a buffer straight into LDS: lane l's bytes land at
-// lds + 16 l. Written out because the compiler makes every later LDS read
-// wait for such loads, also those of the other half of a double buffer; the
-// wait is in sync_stage below. Nothing else here lives in m0: the compiler
-// sets it right before each of its own uses.
+// m0 + 16 l. Written out because the compiler makes every later LDS read wait
+// for such loads, also those of the other half of a double buffer; the wait
+// is in sync_stage below. Nothing else here lives in m0: the compiler sets it
+// right before each of its own uses. An instruction has to stand between the
+// write of m0 and the load: load_to_lds brings one, between set_lds and
+// load_lds the caller has a product.
+__device__ __forceinline__ void set_lds(uint32_t base, uint32_t offset) {
+  asm volatile("s_add_u32 m0, %0, %1" ::"s"(base), "s"(offset) : "scc");
+}
+__device__ __forceinline__ void load_lds(row16_t buffer, uint32_t offset) {
+  asm volatile("buffer_load_dwordx4 %0, %1, 0 offen lds" ::"v"(offset), "s"(buffer) : "memory");
+}
 __device__ __forceinline__ void load_to_lds(row16_t buffer, uint32_t offset, uint32_t lds) {
   asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds" ::"s"(lds),
                "v"(offset), "s"(buffer)
@@ -106,7 +117,7 @@ struct Operand {
   __device__ static __forceinline__ uint32_t source(int i, uint32_t stride, int64_t cols) {
     const int lane = lane_id();
     if constexpr (KMAJOR) {
-      return (uint32_t)(i * 8 + lane / 8) * stride;
+      return (uint32_t)(i * 8 + lane / 8) * stride + chunk_k() * kSize;
     } else {
       const int at = i * 1024 + lane * 16;
       const int k = at / kLine, slot = (at % kLine) / 16;
@@ -121,33 +132,35 @@ struct Operand {
     return ((lane & 7) ^ (lane / 8)) * (16 / kSize);
   }
 
-  // LDS offset of this lane's part of the fragment that starts at row (or
-  // column) `first`, for half `half` of the step's k.
-  __device__ static __forceinline__ uint32_t fragment(int first, int half) {
+  // Fragment f (16 rows or columns from first + 16 f) of half h of the step's
+  // k, for this lane: at(first, K-major ? h : f) plus a constant.
+  static constexpr int addresses(int fragments) { return KMAJOR ? 2 : fragments; }
+  __device__ static __forceinline__ uint32_t at(int first, int index) {
     const int lane = lane_id(), i = lane & 15, q = lane >> 4;
     if constexpr (KMAJOR) {
-      return (first + i) * 128 + (((half * 4 + q) ^ (i & 7)) << 4);
-    } else if constexpr (kSize == 2) {
-      const int k = half * 32 + q * 8 + (i >> 2);
-      return k * kLine + (((first >> 4) ^ swizzle(k)) << 5) + (i & 3) * 8;
+      return (first + i) * 128 + (((index * 4 + q) ^ (i & 7)) << 4);
     } else {
-      const int k = half * 16 + q * 4;
-      return k * kLine + (((first >> 4) ^ swizzle(k)) << 6) + i * 4;
+      const int k = kSize == 2 ? q * 8 + (i >> 2) : q * 4;
+      const int g = ((first >> 4) + index) ^ swizzle(k);
+      return k * kLine + g * (16 * kSize) + (kSize == 2 ? (i & 3) * 8 : i * 4);
     }
   }
-  __device__ static __forceinline__ row16_t read(uint32_t at) {
+  template <int F, int HALF>
+  __device__ static __forceinline__ row16_t read(uint32_t base) {
+    const lds_char* p = (const lds_char*)(uintptr_t)base;
     if constexpr (KMAJOR) {
-      return *reinterpret_cast<__attribute__((address_space(3))) row16_t*>((lds_char*)(uintptr_t)at);
+      return *reinterpret_cast<const __attribute__((address_space(3))) row16_t*>(p + F * 2048);
     } else if constexpr (kSize == 2) {
       typedef __attribute__((address_space(3))) s16x4 lds4;
-      const s16x4 a = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4*)(uintptr_t)at);
-      const s16x4 b = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4*)(uintptr_t)(at + 4 * kLine));
+      constexpr int kHalf = HALF * 32 * kLine;
+      const s16x4 a = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4*)(p + kHalf));
+      const s16x4 b = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4*)(p + kHalf + 4 * kLine));
       return __builtin_bit_cast(row16_t, s16x8{a[0], a[1], a[2], a[3], b[0], b[1], b[2], b[3]});
     } else {
       row16_t v;
       static_for<4>([&](auto t) {
-        v[t.value] = *reinterpret_cast<__attribute__((address_space(3))) uint32_t*>(
-            (lds_char*)(uintptr_t)(at + t * kLine));
+        v[t.value] = *reinterpret_cast<const __attribute__((address_space(3))) uint32_t*>(
+            p + (HALF * 16 + t.value) * kLine);
       });
       return v;
     }
@@ -178,8 +191,10 @@ constexpr int kChunk = 32;
 
 // One block step is a BM x BN tile of C: WM x WN wavefronts, each with a part
 // of (BM / WM) x (BN / WN) in registers as 16 x 16 blocks. Steps of 128 bytes
-// of k go through two LDS buffers: the loads of a step are in flight while
-// the one before is multiplied, one barrier a step.
+// of k go through two LDS buffers and halves of a step through two sets of
+// registers: while a half is multiplied the next one's fragments are read, and
+// a buffer that every wavefront has read out takes the loads of the step after
+// next. One barrier a step, in its middle.
 template <int DT, int P, int BM, int BN, int WM, int WN>
 __global__ void __launch_bounds__(WM* WN* kWave)
     grouped_product_kernel(Dims d, HandleView hv, const void* __restrict__ a,
@@ -214,6 +229,14 @@ __global__ void __launch_bounds__(WM* WN* kWave)
   const int wm = wave / WN, wn = wave % WN;
   const int lane = lane_id();
   const uint32_t lds_base = (uint32_t)(uintptr_t)(lds_char*)lds;
+  using std::integral_constant;
+  // where this wavefront's fragments lie
+  constexpr int kAAt = A::addresses(MF), kBAt = B::addresses(NF);
+  uint32_t a_at[kAAt], b_at[kBAt];
+  static_for<kAAt>([&](auto i) { a_at[i.value] = lds_base + A::at(wm * (BM / WM), i.value); });
+  static_for<kBAt>([&](auto i) {
+    b_at[i.value] = lds_base + A::kBytes + B::at(wn * (BN / WN), i.value);
+  });
   // Blocks are dealt round-robin to the XCDs: chunks of consecutive tiles go
   // to one XCD each in turn. A grid of fewer blocks than tiles (not wgrad)
   // makes a chunk of what an XCD works on at once.
@@ -269,35 +292,53 @@ __global__ void __launch_bounds__(WM* WN* kWave)
       b_off[i] = B::source(wave * BL + i, b_stride, ncols);
     });
 
-    auto load_stage = [&](int step, int buf) {
-      const int32_t k0 = step * A::kDepth;
-      const int32_t left = depth - k0;
-      const int32_t lines = left < A::kDepth ? left : A::kDepth;
-      const uint32_t to = lds_base + buf * kStage;
-      const int chunk = A::chunk_k();
-      const uint32_t ko = chunk < left ? (uint32_t)(k0 + chunk) * kSize : kOutside;
-      if constexpr (P != kWeightGrad) {
-        const row16_t r = buffer_of(a_src, (uint32_t)mrows * a_stride);
-        static_for<AL>([&](auto i) {
-          load_to_lds(r, a_off[i] + ko, to + (wave * AL + i) * 1024);
-        });
-      } else {
-        const row16_t r = buffer_of(a_src + (int64_t)k0 * a_stride, (uint32_t)lines * a_stride);
-        static_for<AL>([&](auto i) {
-          load_to_lds(r, a_off[i], to + (wave * AL + i) * 1024);
-        });
+    // The sources of step k, for the AL + BL loads of this wavefront. Steps
+    // past the last have empty buffers: their loads put zeros into LDS.
+    struct Stage {
+      row16_t a, b;
+      uint32_t to;
+    };
+    auto stage_of = [&](int k) {
+      const int32_t k0 = k * A::kDepth, left = depth - k0;
+      const uint32_t lines = left < 0 ? 0 : left < A::kDepth ? left : A::kDepth;
+      if (left > 0 && left < A::kDepth && P != kWeightGrad) {
+        // the last step: chunks past the end of a row are taken out
+        const uint32_t out = A::chunk_k() < left ? 0 : kOutside;
+        static_for<AL>([&](auto i) { a_off[i] |= out; });
+        if constexpr (P == kForward) static_for<BL>([&](auto i) { b_off[i] |= out; });
       }
-      if constexpr (P == kForward) {
-        const row16_t r = buffer_of(b_src, (uint32_t)ncols * b_stride);
-        static_for<BL>([&](auto i) {
-          load_to_lds(r, b_off[i] + ko, to + A::kBytes + (wave * BL + i) * 1024);
-        });
+      const uint32_t byte0 = (uint32_t)k0 * kSize;
+      Stage g;
+      g.a = P == kWeightGrad
+                ? buffer_of(a_src + (int64_t)k0 * a_stride, lines * a_stride)
+                : buffer_of(a_src + byte0, left > 0 ? (uint32_t)mrows * a_stride - byte0 : 0);
+      g.b = P == kForward
+                ? buffer_of(b_src + byte0, left > 0 ? (uint32_t)ncols * b_stride - byte0 : 0)
+                : buffer_of(b_src + (int64_t)k0 * b_stride, lines * b_stride);
+      g.to = __builtin_amdgcn_readfirstlane(lds_base + (k & 1) * kStage);
+      return g;
+    };
+    // LDS offset, in a stage, of load i
+    auto slot = [&](auto i) -> uint32_t {
+      return i.value < AL ? (wave * AL + i.value) * 1024
+                          : A::kBytes + (wave * BL + i.value - AL) * 1024;
+    };
+    auto load = [&](const Stage& g, auto i) {
+      if constexpr (i.value < AL) {
+        load_lds(g.a, a_off[i.value]);
       } else {
-        const row16_t r = buffer_of(b_src + (int64_t)k0 * b_stride, (uint32_t)lines * b_stride);
-        static_for<BL>([&](auto i) {
-          load_to_lds(r, b_off[i], to + A::kBytes + (wave * BL + i) * 1024);
-        });
+        load_lds(g.b, b_off[i.value - AL]);
       }
+    };
+    auto load_all = [&](const Stage& g, auto from, auto to) {
+      static_for<to.value - from.value>([&](auto n) {
+        constexpr integral_constant<int, from.value + n.value> i{};
+        if constexpr (i.value < AL) {
+          load_to_lds(g.a, a_off[i.value], g.to + slot(i));
+        } else {
+          load_to_lds(g.b, b_off[i.value - AL], g.to + slot(i));
+        }
+      });
     };
 
     f32x4 acc[MF][NF];
@@ -305,26 +346,90 @@ __global__ void __launch_bounds__(WM* WN* kWave)
       static_for<NF>([&](auto j) { acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f}; });
     });
     const bool busy = wm * (BM / WM) < mrows && wn * (BN / WN) < ncols;
-    sync_stage();  // the last tile's reads are done
-    if (steps > 0) load_stage(0, 0);
-    for (int k = 0; k < steps; ++k) {
-      sync_stage();
-      if (k + 1 < steps) load_stage(k + 1, (k + 1) & 1);
-      if (busy) {
-        const uint32_t at = lds_base + (k & 1) * kStage;
-        static_for<2>([&](auto half) {
-          row16_t mf[MF], nf[NF];
-          static_for<NF>([&](auto j) {
-            nf[j] = B::read(at + A::kBytes + B::fragment(wn * (BN / WN) + j * 16, half));
-          });
-          static_for<MF>([&](auto i) {
-            mf[i] = A::read(at + A::fragment(wm * (BM / WM) + i * 16, half));
-          });
-          static_for<MF>([&](auto i) {
-            static_for<NF>([&](auto j) { mma<DT>(acc[i][j], nf[j], mf[i]); });
-          });
-        });
+    // Fragments: the columns' of a half in one of two sets, the rows' in a
+    // ring of four, read two groups of products ahead.
+    row16_t nf[2][NF], mf[4];
+    auto read_n = [&](int k, auto half, auto f) {
+      const uint32_t base = b_at[P == kForward ? half.value : f.value] + (k & 1) * kStage;
+      nf[half.value][f.value] = B::template read<f.value, half.value>(base);
+    };
+    auto read_m = [&](int k, auto half, auto f) {
+      const uint32_t base = a_at[P != kWeightGrad ? half.value : f.value] + (k & 1) * kStage;
+      mf[(half.value * MF + f.value) % 4] = A::template read<f.value, half.value>(base);
+    };
+    // One group of products: row fragment i of a half with every column's.
+    // before(u) comes ahead of product u.
+    auto products = [&](auto half, auto i, auto&& before) {
+      static_for<NF>([&](auto u) {
+        before(u);
+        mma<DT>(acc[i.value][u.value], nf[half.value][u.value],
+                mf[(half.value * MF + i.value) % 4]);
+        __builtin_amdgcn_sched_barrier(0);
+      });
+    };
+    constexpr integral_constant<int, 0> h0{};
+    constexpr integral_constant<int, 1> h1{};
+    // A stage's loads are issued beside four groups of products, a quarter
+    // each: one load for two products, the first of which sets its place.
+    constexpr int kQuarter = NF / 2, kAll = AL + BL;
+    static_assert(kQuarter * 4 == kAll, "four groups issue a stage's loads");
+    auto loads = [&](const Stage& g, auto quarter, auto u) {
+      constexpr integral_constant<int, quarter.value * kQuarter + u.value / 2> i{};
+      if constexpr (u.value % 2 == 0) {
+        set_lds(g.to, slot(i));
+      } else {
+        load(g, i);
       }
+    };
+    if (steps > 0) {
+      load_all(stage_of(0), h0, integral_constant<int, kAll>{});
+      sync_stage();
+      if (busy) {
+        Stage g = stage_of(1);
+        load_all(g, h0, integral_constant<int, kAll / 2>{});
+        static_for<NF>([&](auto f) { read_n(0, h0, f); });
+        read_m(0, h0, h0);
+        read_m(0, h0, h1);
+        for (int k = 0; k < steps; ++k) {
+          static_for<MF>([&](auto i) {
+            products(h0, i, [&](auto u) {
+              if constexpr (u.value == 0) {
+                if constexpr (i.value + 2 < MF) {
+                  read_m(k, h0, integral_constant<int, i.value + 2>{});
+                } else {
+                  read_m(k, h1, integral_constant<int, i.value + 2 - MF>{});
+                }
+              }
+              constexpr int from = NF * i.value / MF, to = NF * (i.value + 1) / MF;
+              if constexpr (u.value >= 1 && u.value - 1 < to - from)
+                read_n(k, h1, integral_constant<int, from + u.value - 1>{});
+              if constexpr (i.value < 2) loads(g, integral_constant<int, 2 + i.value>{}, u);
+            });
+          });
+          static_for<MF - 2>([&](auto i) {
+            products(h1, i, [&](auto u) {
+              if constexpr (u.value == 0) read_m(k, h1, integral_constant<int, i.value + 2>{});
+            });
+          });
+          // Step k is read out everywhere, step k + 1 has landed.
+          sync_stage();
+          g = stage_of(k + 2);
+          static_for<2>([&](auto i) {
+            products(h1, integral_constant<int, MF - 2 + i.value>{}, [&](auto u) {
+              if constexpr (u.value == 0) read_m(k + 1, h0, i);
+              if constexpr (u.value % 2 == 0)
+                read_n(k + 1, h0, integral_constant<int, (i.value * NF + u.value) / 2>{});
+              loads(g, i, u);
+            });
+          });
+        }
+      } else {
+        for (int k = 0; k < steps; ++k) {
+          load_all(stage_of(k + 1), h0, integral_constant<int, kAll>{});
+          sync_stage();
+        }
+      }
+      sync_stage();  // no load is left in flight, and LDS is free again
     }
     // a lane holds four consecutive columns of one row of each 16 x 16 block
     if (busy) {
