@@ -69,13 +69,20 @@ constexpr uint32_t kOutside = 0x40000000u;
 __device__ __forceinline__ void set_lds(uint32_t base, uint32_t offset) {
   asm volatile("s_add_u32 m0, %0, %1" ::"s"(base), "s"(offset) : "scc");
 }
+// ONCE: the bytes are read by one tile only and need not stay in the caches.
+template <bool ONCE>
 __device__ __forceinline__ void load_lds(row16_t buffer, uint32_t offset) {
-  asm volatile("buffer_load_dwordx4 %0, %1, 0 offen lds" ::"v"(offset), "s"(buffer) : "memory");
+  if constexpr (ONCE) {
+    asm volatile("buffer_load_dwordx4 %0, %1, 0 offen nt lds" ::"v"(offset), "s"(buffer)
+                 : "memory");
+  } else {
+    asm volatile("buffer_load_dwordx4 %0, %1, 0 offen lds" ::"v"(offset), "s"(buffer) : "memory");
+  }
 }
+template <bool ONCE>
 __device__ __forceinline__ void load_to_lds(row16_t buffer, uint32_t offset, uint32_t lds) {
-  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds" ::"s"(lds),
-               "v"(offset), "s"(buffer)
-               : "memory");
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0" ::"s"(lds));
+  load_lds<ONCE>(buffer, offset);
 }
 
 // Every load of this wavefront has landed and every LDS read is done, for
@@ -184,7 +191,7 @@ __device__ __forceinline__ void store4(void* p, int64_t i, f32x4 v) {
 
 // Row tiles of an expert whose column tiles run together: with the columns
 // dealt after them, the tiles in flight on an XCD share both operands.
-constexpr int kGroup = 8;
+constexpr int kGroup = 6;
 // Weight-gradient tiles that go to one XCD together: one for each of its CUs.
 constexpr int kChunk = 32;
 
@@ -195,7 +202,9 @@ constexpr int kChunk = 32;
 // registers: while a half is multiplied the next one's fragments are read, and
 // a buffer that every wavefront has read out takes the loads of the step after
 // next. One barrier a step, in its middle.
-template <int DT, int P, int BM, int BN, int WM, int WN>
+// ONCE: B is expected to be read by one tile alone (a single row tile an
+// expert) and passes by the caches.
+template <int DT, int P, int BM, int BN, int WM, int WN, bool ONCE>
 __global__ void __launch_bounds__(WM* WN* kWave)
     grouped_product_kernel(Dims d, HandleView hv, const void* __restrict__ a,
                            const void* __restrict__ b, void* __restrict__ c, int64_t N) {
@@ -325,18 +334,18 @@ __global__ void __launch_bounds__(WM* WN* kWave)
     };
     auto load = [&](const Stage& g, auto i) {
       if constexpr (i.value < AL) {
-        load_lds(g.a, a_off[i.value]);
+        load_lds<false>(g.a, a_off[i.value]);
       } else {
-        load_lds(g.b, b_off[i.value - AL]);
+        load_lds<ONCE>(g.b, b_off[i.value - AL]);
       }
     };
     auto load_all = [&](const Stage& g, auto from, auto to) {
       static_for<to.value - from.value>([&](auto n) {
         constexpr integral_constant<int, from.value + n.value> i{};
         if constexpr (i.value < AL) {
-          load_to_lds(g.a, a_off[i.value], g.to + slot(i));
+          load_to_lds<false>(g.a, a_off[i.value], g.to + slot(i));
         } else {
-          load_to_lds(g.b, b_off[i.value - AL], g.to + slot(i));
+          load_to_lds<ONCE>(g.b, b_off[i.value - AL], g.to + slot(i));
         }
       });
     };
@@ -450,10 +459,10 @@ __global__ void __launch_bounds__(WM* WN* kWave)
   }
 }
 
-template <int DT, int P, int BM, int BN, int WM, int WN>
+template <int DT, int P, int BM, int BN, int WM, int WN, bool ONCE = false>
 hipError_t launch_tiles(const Dims& d, const HandleView& hv, const void* a, const void* b,
                         void* c, int64_t N, int num_cus, int per_cu, hipStream_t stream) {
-  auto* kernel = grouped_product_kernel<DT, P, BM, BN, WM, WN>;
+  auto* kernel = grouped_product_kernel<DT, P, BM, BN, WM, WN, ONCE>;
   const int64_t cols = P == kForward ? N : d.H;
   const int64_t ct = (cols + BN - 1) / BN;
   // the most row tiles that the routing may need: every route's row, and one
@@ -481,12 +490,26 @@ hipError_t launch_product(const Dims& d, const HandleView& hv, const void* a, co
                           void* c, int64_t N, int num_cus, hipStream_t stream) {
   return with_payload(d.dtype, [&](auto dt) {
     constexpr int DT = decltype(dt)::value;
+    // Rows per expert, were the routes spread evenly; measured at 128 experts,
+    // 2048 inputs and 1536 outputs in bf16.
     const int64_t rows = P == kWeightGrad ? N : d.T * d.K / d.E;
     const int64_t cols = P == kForward ? N : d.H;
     if constexpr (DT != EP_DTYPE_FP32) {
-      if (P == kForward && rows <= 16) return launch_grouped_few(d, hv, a, b, c, N, num_cus, stream);
-      if (rows > 128 && cols > 128)
+      // up to 12 rows: 8 rows 135 us against 188 with the tiles below, 16 rows
+      // 193 against 180 (many experts then have more than its 16 rows a pass)
+      if (P == kForward && rows <= 12)
+        return launch_grouped_few(d, hv, a, b, c, N, num_cus, stream);
+      // 256 x 256 tiles from 129 rows, if they fill the CUs: 192 rows 243 us
+      // against 272, 128 rows 300 against 236; 64 of them (256 rows, 512 x 1024
+      // outputs of 8 experts) 16.5 us against 12.5
+      const int64_t tiles = (rows + 255) / 256 * ((cols + 255) / 256) * d.E;
+      if (rows > 128 && cols > 128 && tiles >= num_cus)
         return launch_tiles<DT, P, 256, 256, 2, 4>(d, hv, a, b, c, N, num_cus, 1, stream);
+      // weights past the caches up to 32 rows: 32 rows 186 us against 191 (row
+      // gradient 149 against 154, at 8 rows 131 against 145), 128 rows 300
+      // against 237
+      if (P != kWeightGrad && rows <= 32)
+        return launch_tiles<DT, P, 128, 128, 2, 2, true>(d, hv, a, b, c, N, num_cus, 2, stream);
     }
     return launch_tiles<DT, P, 128, 128, 2, 2>(d, hv, a, b, c, N, num_cus, 2, stream);
   });
