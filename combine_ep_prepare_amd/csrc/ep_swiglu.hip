@@ -2,9 +2,13 @@
 //   out = silu(gate) * up,  silu(g) = g * s,  s = 1 / (1 + exp(-g)),
 // with gate and up the two halves of a row, and its gradient
 //   d_up = grad * g * s,  d_gate = grad * up * s * (1 + g * (1 - s)).
-// Both are bound by HBM traffic: rows of 3 (forward) or 5 (backward) times
-// the hidden size move once. Everything between the loads and the one
-// rounding at the store is fp32.
+//
+// Both are bound by HBM traffic: 3 (forward) or 5 (backward) times the hidden
+// size a row, each value moved once. Everything between the loads and the one
+// rounding at the store is fp32. For that bound the arithmetic has to stay
+// under about 40 instructions a value, which the library's exp and an IEEE
+// quotient alone pass; exp2 and the reciprocal of the hardware (each within a
+// unit in the last place) leave about a dozen.
 
 #include "ep_experts.h"
 
@@ -14,16 +18,50 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kBlocksPerCU = 8;
+// Vectors of a block step, at least: a block takes as many whole rows at a
+// time as hold them, so that narrow rows fill its lanes too.
+constexpr int kStepVectors = 8 * kThreads;
 
-__device__ __forceinline__ float sigmoid(float g) { return 1.f / (1.f + expf(-g)); }
+// 1 / (1 + exp(-g)). The product with log2(e) is rounded, so exp(-g) is off by
+// |g| / 2 units in its last place at most besides the hardware's own one;
+// below g = -88 it is infinite and the result 0.
+__device__ __forceinline__ float sigmoid(float g) {
+  return __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(g * -1.44269504088896340736f));
+}
 
-// A wavefront step is one 1 KiB piece of an output row (or of each half of a
-// gradient row). Rows are taken in address order; row_src tells which hold a
-// route, the others are zeroed under the layout's pad and tail policies.
+// Rounds like Payload::pack; where no lane has a NaN, by the hardware's packed
+// conversions.
+template <int DT, int N>
+__device__ __forceinline__ row16_t pack(const float (&o)[N]) {
+  if constexpr (DT != EP_DTYPE_FP32) {
+    bool nan = false;
+    static_for<N / 2>([&](auto j) { nan |= __builtin_isunordered(o[2 * j], o[2 * j + 1]); });
+    if (wave_ballot(nan) == 0) {
+      typedef std::conditional_t<DT == EP_DTYPE_BF16, __bf16, _Float16> half;
+      typedef half half2 __attribute__((ext_vector_type(2)));
+      typedef float float2v __attribute__((ext_vector_type(2)));
+      row16_t v;
+      static_for<4>([&](auto j) {
+        float2v f = {o[2 * j], o[2 * j + 1]};
+        // the fp32 results stand as they are: no fusing of the last product
+        // with the conversion, which would skip its rounding
+        asm("" : "+v"(f));
+        v[j.value] = __builtin_bit_cast(uint32_t, __builtin_convertvector(f, half2));
+      });
+      return v;
+    }
+  }
+  return Payload<DT>::pack(o);
+}
+
+// A thread takes 16 bytes of each half of a row. Rows are dealt in address
+// order; row_src tells which hold a route, the others are zeroed under the
+// layout's pad and tail policies. row_src is read one step ahead.
 template <int DT, bool BWD>
 __global__ void __launch_bounds__(kThreads)
     swiglu_kernel(Dims d, HandleView hv, const row16_t* __restrict__ grad,
-                  const row16_t* __restrict__ gate_up, row16_t* __restrict__ out) {
+                  const row16_t* __restrict__ gate_up, row16_t* __restrict__ out,
+                  int32_t step_rows) {
   const HandleHeader hh = *hv.header;
   if (!handle_matches(hh, d)) {
     if (blockIdx.x == 0 && threadIdx.x == 0) atomicOr(&hv.header->status, EP_STATUS_LAYOUT);
@@ -33,39 +71,56 @@ __global__ void __launch_bounds__(kThreads)
   constexpr int N = P::N;
   const int64_t live = hh.total < d.cap ? hh.total : d.cap;
   const int64_t rows = d.zero_tail ? d.cap : live;
-  const int64_t V = d.V, pieces = (V + kWave - 1) / kWave;
-  const int waves = kThreads / kWave;
-  for (int64_t i = (int64_t)blockIdx.x * waves + threadIdx.x / kWave; i < rows * pieces;
-       i += (int64_t)gridDim.x * waves) {
-    const int64_t r = i / pieces, v = (i - r * pieces) * kWave + lane_id();
-    const bool held = r < live && hv.row_src[r] >= 0;
-    if (!held && r < live && !d.fill_pads) continue;
-    if (v >= V) continue;
-    row16_t a = {0, 0, 0, 0}, b = {0, 0, 0, 0};
-    if (held) {
-      const row16_t gv = gate_up[r * 2 * V + v], uv = gate_up[r * 2 * V + V + v];
-      row16_t dv = {0, 0, 0, 0};
-      if constexpr (BWD) dv = grad[r * V + v];
-      float o[N], o2[N];
-      static_for<N>([&](auto j) {
-        const float g = P::template get<j>(gv), u = P::template get<j>(uv);
-        const float s = sigmoid(g);
+  const int32_t V = (int32_t)d.V;
+  // the thread's first place in a block step, and the way to its next one
+  const int32_t row_first = threadIdx.x / V, v_first = threadIdx.x % V;
+  const int32_t row_by = kThreads / V, v_by = kThreads % V;
+  for (int64_t r0 = (int64_t)blockIdx.x * step_rows; r0 < rows;
+       r0 += (int64_t)gridDim.x * step_rows) {
+    const int64_t r1 = r0 + step_rows < rows ? r0 + step_rows : rows;
+    int64_t r = r0 + row_first;
+    int32_t v = v_first;
+    int32_t source = r < r1 && r < live ? hv.row_src[r] : -1;
+    while (r < r1) {
+      int64_t next_r = r + row_by;
+      int32_t next_v = v + v_by;
+      if (next_v >= V) {
+        next_v -= V;
+        ++next_r;
+      }
+      const int32_t next_source = next_r < r1 && next_r < live ? hv.row_src[next_r] : -1;
+      row16_t a = {0, 0, 0, 0}, b = {0, 0, 0, 0};
+      if (source >= 0) {
+        const row16_t gv = __builtin_nontemporal_load(gate_up + r * 2 * V + v);
+        const row16_t uv = __builtin_nontemporal_load(gate_up + r * 2 * V + V + v);
+        row16_t dv = {0, 0, 0, 0};
+        if constexpr (BWD) dv = __builtin_nontemporal_load(grad + r * V + v);
+        float o[N], o2[N];
+        static_for<N>([&](auto j) {
+          const float g = P::template get<j>(gv), u = P::template get<j>(uv);
+          const float s = sigmoid(g);
+          if constexpr (BWD) {
+            const float dd = P::template get<j>(dv);
+            o[j] = dd * u * (s * __builtin_fmaf(g, 1.f - s, 1.f));
+            o2[j] = dd * (g * s);
+          } else {
+            o[j] = g * s * u;
+          }
+        });
+        a = pack<DT>(o);
+        if constexpr (BWD) b = pack<DT>(o2);
+      }
+      if (source >= 0 || r >= live || d.fill_pads) {
         if constexpr (BWD) {
-          const float dd = P::template get<j>(dv);
-          o[j] = dd * u * (s * (1.f + g * (1.f - s)));
-          o2[j] = dd * (g * s);
+          store_stream16(out + r * 2 * V + v, a);
+          store_stream16(out + r * 2 * V + V + v, b);
         } else {
-          o[j] = g * s * u;
+          store_stream16(out + r * V + v, a);
         }
-      });
-      a = P::pack(o);
-      if constexpr (BWD) b = P::pack(o2);
-    }
-    if constexpr (BWD) {
-      store_stream16(out + r * 2 * V + v, a);
-      store_stream16(out + r * 2 * V + V + v, b);
-    } else {
-      store_stream16(out + r * V + v, a);
+      }
+      r = next_r;
+      v = next_v;
+      source = next_source;
     }
   }
 }
@@ -74,15 +129,22 @@ __global__ void __launch_bounds__(kThreads)
 
 hipError_t launch_swiglu(const Dims& d, const HandleView& hv, bool backward, const void* grad,
                          const void* gate_up, void* out, int num_cus, hipStream_t stream) {
+  const int32_t step_rows = (int32_t)((kStepVectors + d.V - 1) / d.V);
+  int64_t blocks = (d.cap + step_rows - 1) / step_rows;
+  const int64_t most = (int64_t)num_cus * kBlocksPerCU;
+  if (blocks > most) blocks = most;
+  if (blocks < 1) blocks = 1;
   return with_payload(d.dtype, [&](auto dt) {
-    const dim3 grid(num_cus * kBlocksPerCU), block(kThreads);
+    const dim3 grid((uint32_t)blocks), block(kThreads);
     const row16_t* g = static_cast<const row16_t*>(grad);
     const row16_t* gu = static_cast<const row16_t*>(gate_up);
     row16_t* o = static_cast<row16_t*>(out);
     if (backward) {
-      swiglu_kernel<decltype(dt)::value, true><<<grid, block, 0, stream>>>(d, hv, g, gu, o);
+      swiglu_kernel<decltype(dt)::value, true>
+          <<<grid, block, 0, stream>>>(d, hv, g, gu, o, step_rows);
     } else {
-      swiglu_kernel<decltype(dt)::value, false><<<grid, block, 0, stream>>>(d, hv, g, gu, o);
+      swiglu_kernel<decltype(dt)::value, false>
+          <<<grid, block, 0, stream>>>(d, hv, g, gu, o, step_rows);
     }
     return hipGetLastError();
   });
