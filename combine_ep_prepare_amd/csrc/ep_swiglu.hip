@@ -17,7 +17,7 @@ namespace epmi {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kBlocksPerCU = 8;
+constexpr int kBlocksPerCU = 64;
 // Vectors of a block step, at least: a block takes as many whole rows at a
 // time as hold them, so that narrow rows fill its lanes too.
 constexpr int kStepVectors = 8 * kThreads;
