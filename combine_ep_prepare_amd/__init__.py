@@ -205,14 +205,19 @@ def handle_maps(layout: Layout, handle: torch.Tensor) -> dict:
     }
 
 
-def _ptr(t: Optional[torch.Tensor]):
-    return None if t is None else C.c_void_p(t.data_ptr())
+# The checks below run for every tensor of every call, and the small calls of
+# decoding take about as long on the host as on the GPU: plain ints for
+# pointers (the argument types convert them), one query each for a tensor's
+# device and the current one.
+
+def _ptr(t: Optional[torch.Tensor]) -> Optional[int]:
+    return None if t is None else t.data_ptr()
 
 
-def _stream(stream) -> C.c_void_p:
+def _stream(stream) -> int:
     if stream is None:
-        stream = torch.cuda.current_stream()
-    return C.c_void_p(stream.cuda_stream)
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+    return stream.cuda_stream
 
 
 def _need(t: Optional[torch.Tensor], name: str, dtype, shape=None, allow_none=False):
@@ -222,14 +227,15 @@ def _need(t: Optional[torch.Tensor], name: str, dtype, shape=None, allow_none=Fa
         raise ValueError(f"{name} is required")
     if t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if not t.is_cuda:
+    device = t.get_device()
+    if device < 0 or not t.is_cuda:
         raise ValueError(f"{name} must be a GPU tensor")
-    if t.device.index != torch.cuda.current_device():
+    if device != torch.cuda.current_device():
         raise ValueError(f"{name} is on {t.device}; the library runs on the current device "
                          f"cuda:{torch.cuda.current_device()}")
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
-    if shape is not None and tuple(t.shape) != tuple(shape):
+    if shape is not None and t.shape != shape:
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
 
 

@@ -130,6 +130,11 @@ SHAPES = [
     ("any", 1100, 2, 4, 128, 328, 776),
     ("one", 515, 2, 2, 1, 72, 264),
     ("any", 640, 1, 2048, 1, 64, 64),
+    # enough tiles for the larger ones: a few rows an expert, some, more than 128
+    ("any", 700, 2, 64, 1, 648, 520),
+    ("masked", 1300, 2, 64, 8, 520, 648),
+    ("any", 8400, 2, 112, 1, 520, 520),
+    ("steep", 9000, 2, 112, 4, 520, 776),
 ]
 IDS = [f"{s[0]}-T{s[1]}E{s[3]}H{s[5]}N{s[6]}" for s in SHAPES]
 
@@ -589,6 +594,69 @@ def test_captured_and_replayed():
         torch.cuda.synchronize()
         for k, (a, b) in enumerate(zip(o, o2)):
             assert torch.equal(a, b), (i, k)
+
+
+def test_captured_training_step():
+    """A whole autograd step in one graph: the leaves' gradients after each
+    replay against an eager step on the same values."""
+    T, K, E, A, H, I = 96, 2, 6, 8, 128, 64
+    gen = torch.Generator(device="cuda").manual_seed(2)
+    x = torch.empty(T, H, dtype=torch.bfloat16, device="cuda")
+    w = torch.empty(T, K, device="cuda")
+    idx = torch.empty(T, K, dtype=torch.int64, device="cuda")
+    weights = [(torch.randn(E, a, b, device="cuda", generator=gen) * b ** -0.5).bfloat16()
+               for a, b in ((2 * I, H), (H, I))]
+
+    def fill(i):
+        idx.copy_(torch.from_numpy(route(("any", "masked", "steep")[i % 3], T, K, E, i)))
+        x.normal_(generator=gen)
+        w.uniform_(generator=gen)
+
+    def leaves():
+        return [x.detach().clone().requires_grad_(), w.detach().clone().requires_grad_(),
+                *(p.clone().requires_grad_() for p in weights)]
+
+    def grads(ls):
+        y = _mlp(ls[0], ls[1], idx, ls[2], ls[3], E, A, H)
+        return torch.autograd.grad(y.float().square().sum(), ls)
+
+    fill(0)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        grads(leaves())
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        captured = grads(leaves())
+    for i in range(1, 7):
+        fill(i)
+        graph.replay()
+        torch.cuda.synchronize()
+        for k, (a, b) in enumerate(zip(captured, grads(leaves()))):
+            assert torch.equal(a, b), (i, k)
+
+
+def test_two_streams_at_once():
+    """Two routings' products in flight on two streams, in each kernel that a
+    product may take."""
+    H, N = 264, 520
+    cases = [Case(kind, T, 2, E, 4, "bf16", seed=T, zero_tail=True)
+             for kind, T, E in (("any", 40, 8), ("steep", 900, 8), ("any", 8400, 112))]
+    for c in cases:
+        c.x, c.w = c.buffer(H).cuda(), c.weight(c.E, N, H).cuda()
+        c.alone = c.out(c.cap, N)
+        ep.grouped_linear(c.layout(H), c.handle, c.x, c.w, c.alone)
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in cases]
+    outs = [[c.out(c.cap, N) for _ in range(3)] for c in cases]
+    torch.cuda.synchronize()
+    for i in range(3):
+        for c, st, o in zip(cases, streams, outs):
+            ep.grouped_linear(c.layout(H), c.handle, c.x, c.w, o[i], stream=st)
+    torch.cuda.synchronize()
+    for c, o in zip(cases, outs):
+        assert all(torch.equal(t, c.alone) for t in o)
 
 
 def test_custom_ops_match_the_binding():
