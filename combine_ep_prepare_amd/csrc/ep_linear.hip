@@ -85,10 +85,11 @@ __device__ __forceinline__ void load_to_lds(row16_t buffer, uint32_t offset, uin
   load_lds<ONCE>(buffer, offset);
 }
 
-// Every load of this wavefront has landed and every LDS read is done, for
-// all wavefronts of the block.
-__device__ __forceinline__ void sync_stage() {
-  asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+// For all wavefronts of the block: every LDS read is done, and every load
+// to LDS but the LATEST youngest of each has landed.
+template <int LATEST>
+__device__ __forceinline__ void sync_loads() {
+  asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(LATEST) : "memory");
 }
 
 // One operand's tile of a step: R rows (or columns) by 128 bytes of k, i.e.
@@ -103,7 +104,7 @@ __device__ __forceinline__ void sync_stage() {
 // fp32 one value a lane; f spreads the lines that one read touches.
 // The swizzles are applied to the global side of the loads, whose LDS side is
 // linear.
-template <int DT, bool KMAJOR, int R>
+template <int DT, bool KMAJOR, int R, int EVERY>
 struct Operand {
   static constexpr int kSize = DT == EP_DTYPE_FP32 ? 4 : 2;
   static constexpr int kBytes = R * 128;
@@ -139,8 +140,8 @@ struct Operand {
     return ((lane & 7) ^ (lane / 8)) * (16 / kSize);
   }
 
-  // Fragment f (16 rows or columns from first + 16 f) of half h of the step's
-  // k, for this lane: at(first, K-major ? h : f) plus a constant.
+  // Fragment f (16 rows or columns from first + 16 f EVERY) of half h of the
+  // step's k, for this lane: at(first, K-major ? h : f) plus a constant.
   static constexpr int addresses(int fragments) { return KMAJOR ? 2 : fragments; }
   __device__ static __forceinline__ uint32_t at(int first, int index) {
     const int lane = lane_id(), i = lane & 15, q = lane >> 4;
@@ -148,7 +149,7 @@ struct Operand {
       return (first + i) * 128 + (((index * 4 + q) ^ (i & 7)) << 4);
     } else {
       const int k = kSize == 2 ? q * 8 + (i >> 2) : q * 4;
-      const int g = ((first >> 4) + index) ^ swizzle(k);
+      const int g = ((first >> 4) + index * EVERY) ^ swizzle(k);
       return k * kLine + g * (16 * kSize) + (kSize == 2 ? (i & 3) * 8 : i * 4);
     }
   }
@@ -156,7 +157,7 @@ struct Operand {
   __device__ static __forceinline__ row16_t read(uint32_t base) {
     const lds_char* p = (const lds_char*)(uintptr_t)base;
     if constexpr (KMAJOR) {
-      return *reinterpret_cast<const __attribute__((address_space(3))) row16_t*>(p + F * 2048);
+      return *reinterpret_cast<const __attribute__((address_space(3))) row16_t*>(p + F * EVERY * 2048);
     } else if constexpr (kSize == 2) {
       typedef __attribute__((address_space(3))) s16x4 lds4;
       constexpr int kHalf = HALF * 32 * kLine;
@@ -196,23 +197,32 @@ constexpr int kGroup = 6;
 constexpr int kChunk = 32;
 
 
-// One block step is a BM x BN tile of C: WM x WN wavefronts, each with a part
-// of (BM / WM) x (BN / WN) in registers as 16 x 16 blocks. Steps of 128 bytes
-// of k go through two LDS buffers and halves of a step through two sets of
-// registers: while a half is multiplied the next one's fragments are read, and
-// a buffer that every wavefront has read out takes the loads of the step after
-// next. One barrier a step, in its middle.
+// One block step is a BM x BN tile of C: WM x WN wavefronts, each with every
+// WM-th block of 16 rows and BN / WN columns in registers as 16 x 16 blocks.
+// Steps of 128 bytes of k go through two LDS buffers. What comes from the L2
+// and beyond takes longer than a step, so a buffer's parts (two halves of the
+// rows' operand, the columns') are loaded again each as soon as every
+// wavefront has read it out, and waited for a step and a half later: two
+// barriers a step, neither of which waits for all loads. Waiting for a whole
+// buffer once a step ran at 1353 TFLOP/s on operands of zeros and 1225 on
+// random ones against 1535 and 1274 now (bf16, 32768 rows of 8 experts, 14336
+// inputs, 4096 outputs; a library product of that size 1850 and 1560). The
+// clock falls with the operands' bits: on random ones power is the bound.
+// Eight wavefronts for the large tile, two a SIMD, so that one's products
+// cover the other's LDS reads and barriers; four with twice the columns each
+// read a third less from LDS but ran at 1162.
 // ONCE: B is expected to be read by one tile alone (a single row tile an
 // expert) and passes by the caches.
 template <int DT, int P, int BM, int BN, int WM, int WN, bool ONCE>
 __global__ void __launch_bounds__(WM* WN* kWave)
     grouped_product_kernel(Dims d, HandleView hv, const void* __restrict__ a,
                            const void* __restrict__ b, void* __restrict__ c, int64_t N) {
-  using A = Operand<DT, P != kWeightGrad, BM>;
-  using B = Operand<DT, P == kForward, BN>;
+  // the rows' operand in two halves, the columns' whole
+  using A = Operand<DT, P != kWeightGrad, BM / 2, WM>;
+  using B = Operand<DT, P == kForward, BN, 1>;
   constexpr int kWaves = WM * WN, kThreads = kWaves * kWave;
   constexpr int MF = BM / WM / 16, NF = BN / WN / 16;
-  constexpr int kStage = A::kBytes + B::kBytes;
+  constexpr int kStage = 2 * A::kBytes + B::kBytes;
   constexpr int AL = A::kLoads / kWaves, BL = B::kLoads / kWaves;
   static_assert(AL * kWaves == A::kLoads && BL * kWaves == B::kLoads, "whole loads");
   extern __shared__ __align__(1024) char lds[];
@@ -240,11 +250,11 @@ __global__ void __launch_bounds__(WM* WN* kWave)
   const uint32_t lds_base = (uint32_t)(uintptr_t)(lds_char*)lds;
   using std::integral_constant;
   // where this wavefront's fragments lie
-  constexpr int kAAt = A::addresses(MF), kBAt = B::addresses(NF);
+  constexpr int kAAt = A::addresses(MF / 2), kBAt = B::addresses(NF);
   uint32_t a_at[kAAt], b_at[kBAt];
-  static_for<kAAt>([&](auto i) { a_at[i.value] = lds_base + A::at(wm * (BM / WM), i.value); });
+  static_for<kAAt>([&](auto i) { a_at[i.value] = lds_base + A::at(wm * 16, i.value); });
   static_for<kBAt>([&](auto i) {
-    b_at[i.value] = lds_base + A::kBytes + B::at(wn * (BN / WN), i.value);
+    b_at[i.value] = lds_base + 2 * A::kBytes + B::at(wn * (BN / WN), i.value);
   });
   // Blocks are dealt round-robin to the XCDs: chunks of consecutive tiles go
   // to one XCD each in turn. A grid of fewer blocks than tiles (not wgrad)
@@ -293,60 +303,60 @@ __global__ void __launch_bounds__(WM* WN* kWave)
       b_src += (int64_t)e * N * b_stride + (P == kForward ? n0 * b_stride : n0 * kSize);
     }
     const int steps = (depth + A::kDepth - 1) / A::kDepth;
-    uint32_t a_off[AL], b_off[BL];
+    uint32_t a_off[2][AL], b_off[BL];
     static_for<AL>([&](auto i) {
-      a_off[i] = A::source(wave * AL + i, a_stride, mrows);
+      static_for<2>([&](auto h) {
+        a_off[h][i] = A::source(wave * AL + i, a_stride, mrows - h * (BM / 2));
+      });
     });
-    static_for<BL>([&](auto i) {
-      b_off[i] = B::source(wave * BL + i, b_stride, ncols);
-    });
+    static_for<BL>([&](auto i) { b_off[i] = B::source(wave * BL + i, b_stride, ncols); });
 
-    // The sources of step k, for the AL + BL loads of this wavefront. Steps
-    // past the last have empty buffers: their loads put zeros into LDS.
-    struct Stage {
-      row16_t a, b;
+    // A part (0, 1: the halves of A, 2: B) of step k: its source and its place
+    // in LDS. A step past the last has an empty buffer: its loads put zeros into
+    // LDS.
+    struct Part {
+      row16_t buffer;
       uint32_t to;
     };
-    auto stage_of = [&](int k) {
+    auto part_of = [&](auto part, int k) {
+      constexpr bool kRows = part.value < 2;
+      constexpr bool kMajor = kRows ? P != kWeightGrad : P == kForward;
+      constexpr int n = kRows ? AL : BL;
+      constexpr int kSkip = kRows ? part.value * (BM / 2) : 0;  // rows before the part
+      uint32_t* off = kRows ? a_off[part.value & 1] : b_off;
       const int32_t k0 = k * A::kDepth, left = depth - k0;
-      const uint32_t lines = left < 0 ? 0 : left < A::kDepth ? left : A::kDepth;
-      if (left > 0 && left < A::kDepth && P != kWeightGrad) {
-        // the last step: chunks past the end of a row are taken out
-        const uint32_t out = A::chunk_k() < left ? 0 : kOutside;
-        static_for<AL>([&](auto i) { a_off[i] |= out; });
-        if constexpr (P == kForward) static_for<BL>([&](auto i) { b_off[i] |= out; });
-      }
-      const uint32_t byte0 = (uint32_t)k0 * kSize;
-      Stage g;
-      g.a = P == kWeightGrad
-                ? buffer_of(a_src + (int64_t)k0 * a_stride, lines * a_stride)
-                : buffer_of(a_src + byte0, left > 0 ? (uint32_t)mrows * a_stride - byte0 : 0);
-      g.b = P == kForward
-                ? buffer_of(b_src + byte0, left > 0 ? (uint32_t)ncols * b_stride - byte0 : 0)
-                : buffer_of(b_src + (int64_t)k0 * b_stride, lines * b_stride);
-      g.to = __builtin_amdgcn_readfirstlane(lds_base + (k & 1) * kStage);
-      return g;
-    };
-    // LDS offset, in a stage, of load i
-    auto slot = [&](auto i) -> uint32_t {
-      return i.value < AL ? (wave * AL + i.value) * 1024
-                          : A::kBytes + (wave * BL + i.value - AL) * 1024;
-    };
-    auto load = [&](const Stage& g, auto i) {
-      if constexpr (i.value < AL) {
-        load_lds<false>(g.a, a_off[i.value]);
-      } else {
-        load_lds<ONCE>(g.b, b_off[i.value - AL]);
-      }
-    };
-    auto load_all = [&](const Stage& g, auto from, auto to) {
-      static_for<to.value - from.value>([&](auto n) {
-        constexpr integral_constant<int, from.value + n.value> i{};
-        if constexpr (i.value < AL) {
-          load_to_lds<false>(g.a, a_off[i.value], g.to + slot(i));
-        } else {
-          load_to_lds<ONCE>(g.b, b_off[i.value - AL], g.to + slot(i));
+      const uint32_t stride = kRows ? a_stride : b_stride;
+      const int32_t held = (kRows ? mrows : ncols) - kSkip;   // rows or columns of the part
+      const char* src = kRows ? a_src : b_src;
+      Part p;
+      if constexpr (kMajor) {
+        if (left > 0 && left < A::kDepth) {
+          // the last step: chunks past the end of a row are taken out
+          const uint32_t out = A::chunk_k() < left ? 0 : kOutside;
+          static_for<n>([&](auto i) { off[i] |= out; });
         }
+        const uint32_t byte0 = (uint32_t)k0 * kSize;
+        p.buffer = buffer_of(src + (int64_t)kSkip * stride + byte0,
+                             left > 0 && held > 0 ? (uint32_t)held * stride - byte0 : 0);
+      } else {
+        const uint32_t lines = left < 0 ? 0 : left < A::kDepth ? left : A::kDepth;
+        p.buffer = buffer_of(src + (int64_t)k0 * stride + kSkip * kSize,
+                             lines > 0 && held > 0 ? lines * stride - kSkip * kSize : 0);
+      }
+      p.to = __builtin_amdgcn_readfirstlane(lds_base + (k & 1) * kStage +
+                                            part.value * A::kBytes + wave * n * 1024);
+      return p;
+    };
+    auto load_at = [&](auto part, const Part& p, auto i) {   // m0 is set
+      load_lds<(part.value == 2 && ONCE)>(
+          p.buffer, part.value == 2 ? b_off[i.value] : a_off[part.value & 1][i.value]);
+    };
+    auto load_part = [&](auto part, int k) {
+      const Part p = part_of(part, k);
+      static_for<part.value == 2 ? BL : AL>([&](auto i) {
+        load_to_lds<(part.value == 2 && ONCE)>(
+            p.buffer, part.value == 2 ? b_off[i.value] : a_off[part.value & 1][i.value],
+            p.to + i.value * 1024);
       });
     };
 
@@ -354,96 +364,121 @@ __global__ void __launch_bounds__(WM* WN* kWave)
     static_for<MF>([&](auto i) {
       static_for<NF>([&](auto j) { acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f}; });
     });
-    const bool busy = wm * (BM / WM) < mrows && wn * (BN / WN) < ncols;
-    // Fragments: the columns' of a half in one of two sets, the rows' in a
-    // ring of four, read two groups of products ahead.
+    // Fragments: the columns' of both halves of k, the rows' in a ring of four,
+    // read kAhead groups of products ahead. Group g of a step is row fragment
+    // g / 2 with half g % 2 of k, times every column fragment.
+    constexpr int kAhead = MF >= 4 ? 3 : 1;
+    constexpr int kGroups = 2 * MF, kMid = MF - kAhead, kEnd = kGroups - kAhead;
     row16_t nf[2][NF], mf[4];
     auto read_n = [&](int k, auto half, auto f) {
       const uint32_t base = b_at[P == kForward ? half.value : f.value] + (k & 1) * kStage;
       nf[half.value][f.value] = B::template read<f.value, half.value>(base);
     };
-    auto read_m = [&](int k, auto half, auto f) {
-      const uint32_t base = a_at[P != kWeightGrad ? half.value : f.value] + (k & 1) * kStage;
-      mf[(half.value * MF + f.value) % 4] = A::template read<f.value, half.value>(base);
+    auto read_m = [&](int k, auto g) {
+      constexpr int half = g.value % 2, f = g.value / 2 % (MF / 2), part = g.value / MF;
+      const uint32_t base =
+          a_at[P != kWeightGrad ? half : f] + (k & 1) * kStage + part * A::kBytes;
+      mf[g.value % 4] = A::template read<f, half>(base);
     };
-    // One group of products: row fragment i of a half with every column's.
-    // before(u) comes ahead of product u.
-    auto products = [&](auto half, auto i, auto&& before) {
-      static_for<NF>([&](auto u) {
-        before(u);
-        mma<DT>(acc[i.value][u.value], nf[half.value][u.value],
-                mf[(half.value * MF + i.value) % 4]);
-        __builtin_amdgcn_sched_barrier(0);
+    constexpr integral_constant<int, 0> i0{};
+    constexpr integral_constant<int, 1> i1{};
+    constexpr integral_constant<int, 2> i2{};
+    // One load every kEvery products from product 0 of a stretch on: the first
+    // sets its place, the next one brings it.
+    auto spread = [&](auto part, const Part& p, auto slot, auto first, auto every) {
+      constexpr int at = slot.value - first.value * every.value;
+      constexpr int n = part.value == 2 ? BL : AL;
+      if constexpr (at >= 0 && at / every.value < n) {
+        constexpr integral_constant<int, at / every.value> i{};
+        if constexpr (every.value == 1) {
+          load_to_lds<(part.value == 2 && ONCE)>(
+              p.buffer, part.value == 2 ? b_off[i.value] : a_off[part.value & 1][i.value],
+              p.to + i.value * 1024);
+        } else if constexpr (at % every.value == 0) {
+          set_lds(p.to, i.value * 1024);
+        } else if constexpr (at % every.value == 1) {
+          load_at(part, p, i);
+        }
+      }
+    };
+    // Step k. Two syncs; what is read out at one makes room for loads that are
+    // waited for a step and a half later:
+    //   mid  A's first half of k and B of k are read out, A's second half has landed
+    //   end  A's second half of k is read out, A's first and B of k + 1 have landed
+    // The loads are A0 and B of k + 2 at the mid, A1 of k + 2 at the end: at either
+    // sync all but the 2 AL + BL youngest have to have landed.
+    auto step = [&](auto compute, int k) {
+      Part p0, p1, p2;
+      static_for<kGroups>([&](auto g) {
+        if constexpr (g.value == kMid) {
+          sync_loads<2 * AL + BL>();
+          p0 = part_of(i0, k + 2);
+          p2 = part_of(i2, k + 2);
+        }
+        if constexpr (g.value == kEnd) {
+          sync_loads<2 * AL + BL>();
+          p1 = part_of(i1, k + 2);
+        }
+        if constexpr (compute.value) {
+          constexpr int kMidEvery = (kEnd - kMid) * NF / (AL + BL);
+          constexpr int kEndEvery = kAhead * NF / AL;
+          static_assert(kMidEvery >= 1 && kEndEvery >= 1, "a product for every load");
+          if constexpr (g.value + kAhead < kGroups) {
+            read_m(k, integral_constant<int, g.value + kAhead>{});
+          } else {
+            read_m(k + 1, integral_constant<int, g.value + kAhead - kGroups>{});
+          }
+          static_for<NF>([&](auto u) {
+            // a set of column fragments is read anew as soon as its last use is past
+            if constexpr (g.value == 0) read_n(k, i1, u);
+            if constexpr (g.value == kGroups - 1) read_n(k + 1, i0, u);
+            if constexpr (g.value >= kMid && g.value < kEnd) {
+              constexpr integral_constant<int, (g.value - kMid) * NF + u.value> slot{};
+              spread(i0, p0, slot, i0, integral_constant<int, kMidEvery>{});
+              spread(i2, p2, slot, integral_constant<int, AL>{},
+                     integral_constant<int, kMidEvery>{});
+            }
+            if constexpr (g.value >= kEnd) {
+              constexpr integral_constant<int, (g.value - kEnd) * NF + u.value> slot{};
+              spread(i1, p1, slot, i0, integral_constant<int, kEndEvery>{});
+            }
+            mma<DT>(acc[g.value / 2][u.value], nf[g.value % 2][u.value], mf[g.value % 4]);
+            __builtin_amdgcn_sched_barrier(0);
+          });
+        } else if constexpr (g.value == kMid) {
+          load_part(i0, k + 2);
+          load_part(i2, k + 2);
+        } else if constexpr (g.value == kEnd) {
+          load_part(i1, k + 2);
+        }
       });
     };
-    constexpr integral_constant<int, 0> h0{};
-    constexpr integral_constant<int, 1> h1{};
-    // A stage's loads are issued beside four groups of products, a quarter
-    // each: one load for two products, the first of which sets its place.
-    constexpr int kQuarter = NF / 2, kAll = AL + BL;
-    static_assert(kQuarter * 4 == kAll, "four groups issue a stage's loads");
-    auto loads = [&](const Stage& g, auto quarter, auto u) {
-      constexpr integral_constant<int, quarter.value * kQuarter + u.value / 2> i{};
-      if constexpr (u.value % 2 == 0) {
-        set_lds(g.to, slot(i));
-      } else {
-        load(g, i);
+    auto all_steps = [&](auto compute) {
+      static_for<2>([&](auto k) {
+        load_part(i0, k);
+        load_part(i2, k);
+        load_part(i1, k);
+      });
+      sync_loads<2 * AL + BL>();
+      if constexpr (compute.value) {
+        static_for<NF>([&](auto f) { read_n(0, i0, f); });
+        static_for<kAhead>([&](auto g) { read_m(0, g); });
       }
+      for (int k = 0; k < steps; ++k) step(compute, k);
+      sync_loads<0>();  // no load is left in flight, and LDS is free again
     };
+    const bool busy = wm * 16 < mrows && wn * (BN / WN) < ncols;
     if (steps > 0) {
-      load_all(stage_of(0), h0, integral_constant<int, kAll>{});
-      sync_stage();
       if (busy) {
-        Stage g = stage_of(1);
-        load_all(g, h0, integral_constant<int, kAll / 2>{});
-        static_for<NF>([&](auto f) { read_n(0, h0, f); });
-        read_m(0, h0, h0);
-        read_m(0, h0, h1);
-        for (int k = 0; k < steps; ++k) {
-          static_for<MF>([&](auto i) {
-            products(h0, i, [&](auto u) {
-              if constexpr (u.value == 0) {
-                if constexpr (i.value + 2 < MF) {
-                  read_m(k, h0, integral_constant<int, i.value + 2>{});
-                } else {
-                  read_m(k, h1, integral_constant<int, i.value + 2 - MF>{});
-                }
-              }
-              constexpr int from = NF * i.value / MF, to = NF * (i.value + 1) / MF;
-              if constexpr (u.value >= 1 && u.value - 1 < to - from)
-                read_n(k, h1, integral_constant<int, from + u.value - 1>{});
-              if constexpr (i.value < 2) loads(g, integral_constant<int, 2 + i.value>{}, u);
-            });
-          });
-          static_for<MF - 2>([&](auto i) {
-            products(h1, i, [&](auto u) {
-              if constexpr (u.value == 0) read_m(k, h1, integral_constant<int, i.value + 2>{});
-            });
-          });
-          // Step k is read out everywhere, step k + 1 has landed.
-          sync_stage();
-          g = stage_of(k + 2);
-          static_for<2>([&](auto i) {
-            products(h1, integral_constant<int, MF - 2 + i.value>{}, [&](auto u) {
-              if constexpr (u.value == 0) read_m(k + 1, h0, i);
-              if constexpr (u.value % 2 == 0)
-                read_n(k + 1, h0, integral_constant<int, (i.value * NF + u.value) / 2>{});
-              loads(g, i, u);
-            });
-          });
-        }
+        all_steps(std::true_type{});
       } else {
-        for (int k = 0; k < steps; ++k) {
-          load_all(stage_of(k + 1), h0, integral_constant<int, kAll>{});
-          sync_stage();
-        }
+        all_steps(std::false_type{});
       }
-      sync_stage();  // no load is left in flight, and LDS is free again
     }
     // a lane holds four consecutive columns of one row of each 16 x 16 block
     if (busy) {
       static_for<MF>([&](auto i) {
-        const int32_t m = wm * (BM / WM) + i * 16 + (lane & 15);
+        const int32_t m = (i * WM + wm) * 16 + (lane & 15);
         if (m < mrows) {
           const int64_t r = P == kWeightGrad ? (int64_t)e * N + m0 + m : s.row + m0 + m;
           static_for<NF>([&](auto j) {
@@ -495,29 +530,32 @@ hipError_t launch_product(const Dims& d, const HandleView& hv, const void* a, co
     const int64_t rows = P == kWeightGrad ? N : d.T * d.K / d.E;
     const int64_t cols = P == kForward ? N : d.H;
     if constexpr (DT != EP_DTYPE_FP32) {
-      // up to 12 rows: 8 rows 135 us against 188 with the tiles below, 16 rows
-      // 193 against 180 (many experts then have more than its 16 rows a pass)
+      // up to 12 rows: 8 rows 135 us against 144 with the tiles below, one row 90
+      // against 103; 16 rows 193 against 152 (many experts then have more rows
+      // than the 16 of its pass)
       if (P == kForward && rows <= 12)
         return launch_grouped_few(d, hv, a, b, c, N, num_cus, stream);
-      // 256 x 256 tiles from 129 rows, if they fill the CUs: 192 rows 243 us
-      // against 272, 128 rows 300 against 236; 64 of them (256 rows, 512 x 1024
-      // outputs of 8 experts) 16.5 us against 12.5
+      // 256 x 256 tiles from 129 rows, if they fill the CUs: 192 rows 240 us
+      // against 272, 128 rows 300 against 238
       const int64_t tiles = (rows + 255) / 256 * ((cols + 255) / 256) * d.E;
       if (rows > 128 && cols > 128 && tiles >= num_cus)
         return launch_tiles<DT, P, 256, 256, 2, 4>(d, hv, a, b, c, N, num_cus, 1, stream);
-      // weights past the caches up to 32 rows: 32 rows 186 us against 191 (row
-      // gradient 149 against 154, at 8 rows 131 against 145), 128 rows 300
-      // against 237
-      if (P != kWeightGrad && rows <= 32)
-        return launch_tiles<DT, P, 128, 128, 2, 2, true>(d, hv, a, b, c, N, num_cus, 2, stream);
     }
     // 64 x 64 tiles where larger ones would leave CUs without work (one expert of
-    // 256 rows, 4096 x 4096: 36 us against 44; five of 6150 rows, 224 x 320: 171
-    // against 413 for fp32's weight gradient). fp32 is bound by its matrix
+    // 256 rows, 4096 x 4096: 27 us against 44; fp32's weight gradient of five of
+    // 6150 rows, 224 x 320: 121 against 413). fp32 is bound by its matrix
     // instructions, not by loads, and gains up to four of the larger a CU.
     const int64_t tiles = (rows + 127) / 128 * ((cols + 127) / 128) * d.E;
     if (tiles < (DT == EP_DTYPE_FP32 ? 4 : 1) * num_cus)
       return launch_tiles<DT, P, 64, 64, 2, 2>(d, hv, a, b, c, N, num_cus, 4, stream);
+    if constexpr (DT != EP_DTYPE_FP32) {
+      // weights past the caches up to 64 rows, where nearly all experts have one
+      // row tile: 16 rows 152 us against 166, 64 rows 175 against 180 (row
+      // gradient, 8 rows: 130 against 149); at 128 rows half of them have two
+      if (P != kWeightGrad && rows <= 64)
+        return launch_tiles<DT, P, 128, 128, 2, 2, P != kWeightGrad>(d, hv, a, b, c, N, num_cus,
+                                                                     2, stream);
+    }
     return launch_tiles<DT, P, 128, 128, 2, 2>(d, hv, a, b, c, N, num_cus, 2, stream);
   });
 }
