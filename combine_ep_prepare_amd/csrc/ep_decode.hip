@@ -122,7 +122,7 @@ struct Stream {
   };
 
   row16_t w[kLoads];
-  row16_t x[2][kParts];
+  row16_t x[kParts];                   // of the half that comes next
   uint16_t scale[QUANT ? kRows : 1];   // of column `lane`
   uint8_t zero[QUANT ? kRows : 1];
 
@@ -170,7 +170,7 @@ struct Stream {
       const bool in = !PART || k < H;
       const row16_t v =
           *reinterpret_cast<const row16_t*>(s.x + (s.x_off + (uint32_t)(in ? k : 0) * 2));
-      x[half][t] = in ? v : row16_t{0, 0, 0, 0};
+      x[t] = in ? v : row16_t{0, 0, 0, 0};
     });
   }
 
@@ -242,21 +242,31 @@ struct Stream {
     }
   }
 
-  // Multiplies the loaded step; the next one's loads (step k1 of `next`) are
-  // issued as the registers they fill are done with.
-  template <bool MORE>
-  __device__ __forceinline__ void step(char* lds, const Source& next, int32_t k1, int32_t H,
-                                       uint32_t bits, f32x4 (&acc)[kNF]) {
+  // The first loads of a step from input k0 on: weights, x of its first half.
+  template <bool PART>
+  __device__ __forceinline__ void load(const Source& s, int32_t k0, int32_t H) {
+    load_weights<PART>(s, k0, H);
+    load_x<PART>(s, 0, k0, H);
+  }
+  // Multiplies the loaded step (from input k0 on; the one that passes the end of
+  // the row with PART); with MORE the whole step from input k1 on is loaded as
+  // registers get free. Loads come back in order: x of the second half is asked
+  // for ahead of the next step's weights, which it must not wait for.
+  template <bool PART, bool MORE>
+  __device__ __forceinline__ void step(char* lds, const Source& s, int32_t k0, int32_t k1,
+                                       int32_t H, uint32_t bits, f32x4 (&acc)[kNF]) {
     put(lds);
-    if constexpr (MORE) load_weights<false>(next, k1, H);
-    static_for<2>([&](auto half) {
-      row16_t xs[kParts];
-      static_for<kParts>([&](auto t) {
-        xs[t] = QUANT ? interleave(x[half][t]) : x[half][t];
-      });
-      if constexpr (MORE) load_x<false>(next, half, k1, H);
-      multiply(lds, half, xs, bits, acc);
-    });
+    row16_t xs[kParts];
+    auto take_x = [&]() {
+      static_for<kParts>([&](auto t) { xs[t] = QUANT ? interleave(x[t]) : x[t]; });
+    };
+    take_x();
+    load_x<PART>(s, 1, k0, H);
+    if constexpr (MORE) load_weights<false>(s, k1, H);
+    multiply(lds, 0, xs, bits, acc);
+    take_x();
+    if constexpr (MORE) load_x<false>(s, 0, k1, H);
+    multiply(lds, 1, xs, bits, acc);
   }
 };
 
@@ -278,13 +288,14 @@ __global__ void __launch_bounds__(kThreads, blocks_per_cu(QUANT))
   using S = Stream<DT, QUANT, G, ZEROS>;
   extern __shared__ __align__(16) char mem[];
   int32_t* tile_start = reinterpret_cast<int32_t*>(mem + kWaves * S::kLds);
+  const int32_t my_rows = rows_of_thread(hv, d);
   const HandleHeader hh = *hv.header;
   if (!handle_matches(hh, d)) {
     if (blockIdx.x == 0 && threadIdx.x == 0) atomicOr(&hv.header->status, EP_STATUS_LAYOUT);
     return;
   }
   const int64_t row_tiles =
-      list_tiles<kThreads>(hv, d, kRowTile, tile_start, tile_start + d.E + 1);
+      list_tiles<kThreads>(hv, d, kRowTile, my_rows, tile_start, tile_start + d.E + 1);
   const int64_t ct = (N + kCols - 1) / kCols, tiles = row_tiles * ct;
   const int32_t H = (int32_t)d.H;
   const int lane = lane_id(), i16 = lane & 15;
@@ -324,11 +335,7 @@ __global__ void __launch_bounds__(kThreads, blocks_per_cu(QUANT))
   const int32_t first = wave * S::kStep, stride = kWaves * S::kStep;
   S s;
   auto load = [&](const Place& p) {
-    if (wave < full) {
-      s.template load_weights<false>(p.src, first, H);
-      s.template load_x<false>(p.src, 0, first, H);
-      s.template load_x<false>(p.src, 1, first, H);
-    }
+    if (wave < full) s.template load<false>(p.src, first, H);
   };
   Place next;
   if ((int64_t)blockIdx.x < tiles) {
@@ -342,14 +349,12 @@ __global__ void __launch_bounds__(kThreads, blocks_per_cu(QUANT))
     if (wave < full) {
       int32_t k = first;
       for (; k + stride < full * S::kStep; k += stride)
-        s.template step<true>(lds, cur.src, k + stride, H, bits, acc);
-      s.template step<false>(lds, cur.src, 0, H, bits, acc);
+        s.template step<false, true>(lds, cur.src, k, k + stride, H, bits, acc);
+      s.template step<false, false>(lds, cur.src, k, 0, H, bits, acc);
     }
     if (full * S::kStep < H && wave == kWaves - 1) {
-      s.template load_weights<true>(cur.src, full * S::kStep, H);
-      s.template load_x<true>(cur.src, 0, full * S::kStep, H);
-      s.template load_x<true>(cur.src, 1, full * S::kStep, H);
-      s.template step<false>(lds, cur.src, 0, H, bits, acc);
+      s.template load<true>(cur.src, full * S::kStep, H);
+      s.template step<true, false>(lds, cur.src, full * S::kStep, 0, H, bits, acc);
     }
     if (t + gridDim.x < tiles) {
       next = place(t + gridDim.x);

@@ -27,18 +27,24 @@ __device__ __forceinline__ Segment segment_of(const HandleView& hv, const Dims& 
 }
 
 // tile_start[e] (LDS, E + 1 entries) = the number of row tiles of bm rows
-// before expert e; returns their total. Every thread of the block calls it;
-// part holds one word per wavefront. The barriers inside make the list
-// visible to the whole block.
+// before expert e; returns their total. Every thread of the block calls it
+// with the live rows of expert threadIdx.x, which it has asked for ahead of
+// the handle check (the handle's maps are there whatever they hold); part
+// holds one word per wavefront. The barriers inside make the list visible to
+// the whole block.
+__device__ __forceinline__ int32_t rows_of_thread(const HandleView& hv, const Dims& d) {
+  return (int)threadIdx.x < d.E ? segment_of(hv, d, (int)threadIdx.x).rows : 0;
+}
 template <int THREADS>
 __device__ __forceinline__ int32_t list_tiles(const HandleView& hv, const Dims& d, int bm,
-                                              int32_t* tile_start, int32_t* part) {
+                                              int32_t first_rows, int32_t* tile_start,
+                                              int32_t* part) {
   constexpr int kWaves = THREADS / kWave;
   const int lane = lane_id(), wave = threadIdx.x / kWave;
   int32_t base = 0;
   for (int e0 = 0; e0 < d.E; e0 += THREADS) {
     const int e = e0 + (int)threadIdx.x;
-    const int32_t rows = e < d.E ? segment_of(hv, d, e).rows : 0;
+    const int32_t rows = e0 == 0 ? first_rows : e < d.E ? segment_of(hv, d, e).rows : 0;
     const int32_t tiles = (rows + bm - 1) / bm;
     int32_t sum = tiles;
     static_for<6>([&](auto i) {

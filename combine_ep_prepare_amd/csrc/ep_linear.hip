@@ -40,8 +40,8 @@ __device__ __forceinline__ void mma(f32x4& acc, row16_t n, row16_t m) {
         __builtin_bit_cast(f16x8, n), __builtin_bit_cast(f16x8, m), acc, 0, 0, 0);
   } else {
     static_for<4>([&](auto t) {
-      acc = __builtin_amdgcn_mfma_f32_16x16x4f32(__uint_as_float(n[t.value]), __uint_as_float(m[t.value]),
-                                                 acc, 0, 0, 0);
+      acc = __builtin_amdgcn_mfma_f32_16x16x4f32(__uint_as_float(n[t.value]),
+                                                 __uint_as_float(m[t.value]), acc, 0, 0, 0);
     });
   }
 }
@@ -163,7 +163,8 @@ struct Operand {
       constexpr int kHalf = HALF * 32 * kLine;
       const s16x4 a = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4*)(p + kHalf));
       const s16x4 b = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4*)(p + kHalf + 4 * kLine));
-      return __builtin_bit_cast(row16_t, s16x8{a[0], a[1], a[2], a[3], b[0], b[1], b[2], b[3]});
+      return __builtin_bit_cast(row16_t,
+                                s16x8{a[0], a[1], a[2], a[3], b[0], b[1], b[2], b[3]});
     } else {
       row16_t v;
       static_for<4>([&](auto t) {
@@ -195,7 +196,6 @@ __device__ __forceinline__ void store4(void* p, int64_t i, f32x4 v) {
 constexpr int kGroup = 6;
 // Weight-gradient tiles that go to one XCD together: one for each of its CUs.
 constexpr int kChunk = 32;
-
 
 // One block step is a BM x BN tile of C: WM x WN wavefronts, each with every
 // WM-th block of 16 rows and BN / WN columns in registers as 16 x 16 blocks.
@@ -229,6 +229,7 @@ __global__ void __launch_bounds__(WM* WN* kWave)
   int32_t* tile_start = reinterpret_cast<int32_t*>(lds + 2 * kStage);
   int32_t* part = tile_start + d.E + 1;
 
+  const int32_t my_rows = rows_of_thread(hv, d);
   const HandleHeader hh = *hv.header;
   if (!handle_matches(hh, d)) {
     if (blockIdx.x == 0 && threadIdx.x == 0) atomicOr(&hv.header->status, EP_STATUS_LAYOUT);
@@ -242,7 +243,7 @@ __global__ void __launch_bounds__(WM* WN* kWave)
   if constexpr (P == kWeightGrad) {
     tiles = (int64_t)d.E * nt * ct;
   } else {
-    tiles = (int64_t)list_tiles<kThreads>(hv, d, BM, tile_start, part) * ct;
+    tiles = (int64_t)list_tiles<kThreads>(hv, d, BM, my_rows, tile_start, part) * ct;
   }
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
   const int wm = wave / WN, wn = wave % WN;
