@@ -282,12 +282,17 @@ __global__ void __launch_bounds__(WM* WN* kWave)
     const int32_t group = (int32_t)(in_e / ((int64_t)kGroup * ct));
     const int32_t in_g = (int32_t)(in_e - (int64_t)group * kGroup * ct);
     const int32_t gm = rts - group * kGroup < kGroup ? rts - group * kGroup : kGroup;
-    const int64_t m0 = __builtin_amdgcn_readfirstlane((group * kGroup + in_g % gm) * BM);
+    const int32_t mi = __builtin_amdgcn_readfirstlane(group * kGroup + in_g % gm);
     const int64_t n0 = __builtin_amdgcn_readfirstlane((in_g / gm) * BN);
     const Segment s = segment_of(hv, d, e);
     const int64_t M = P == kWeightGrad ? N : s.rows;
+    // Rows are shared out evenly over a segment's tiles, in blocks of 16: tiles
+    // that start together then stay together, and find each other's operands in
+    // the L2.
+    const int32_t height = (int32_t)(((M + rts - 1) / rts + 15) / 16 * 16);
+    const int64_t m0 = (int64_t)mi * height;
     const int32_t depth = (int32_t)(P == kForward ? H : (P == kRowGrad ? N : s.rows));
-    const int32_t mrows = (int32_t)(M - m0 < BM ? M - m0 : BM);
+    const int32_t mrows = (int32_t)(M - m0 < height ? M - m0 : height);
     const int32_t ncols = (int32_t)(cols - n0 < BN ? cols - n0 : BN);
     constexpr int kSize = A::kSize;
 
@@ -384,17 +389,20 @@ __global__ void __launch_bounds__(WM* WN* kWave)
     constexpr integral_constant<int, 0> i0{};
     constexpr integral_constant<int, 1> i1{};
     constexpr integral_constant<int, 2> i2{};
-    // One load every kEvery products from product 0 of a stretch on: the first
-    // sets its place, the next one brings it.
-    auto spread = [&](auto part, const Part& p, auto slot, auto first, auto every) {
+    // One load every EVERY products of a stretch: the first sets its place, the
+    // next one brings it. Without a product between the two (EVERY 1, or a tile
+    // that leaves some out) both come at once.
+    auto spread = [&](auto part, const Part& p, auto slot, auto first, auto every, auto whole) {
       constexpr int at = slot.value - first.value * every.value;
       constexpr int n = part.value == 2 ? BL : AL;
       if constexpr (at >= 0 && at / every.value < n) {
         constexpr integral_constant<int, at / every.value> i{};
-        if constexpr (every.value == 1) {
-          load_to_lds<(part.value == 2 && ONCE)>(
-              p.buffer, part.value == 2 ? b_off[i.value] : a_off[part.value & 1][i.value],
-              p.to + i.value * 1024);
+        if constexpr (every.value == 1 || !whole.value) {
+          if constexpr (at % every.value == 0) {
+            load_to_lds<(part.value == 2 && ONCE)>(
+                p.buffer, part.value == 2 ? b_off[i.value] : a_off[part.value & 1][i.value],
+                p.to + i.value * 1024);
+          }
         } else if constexpr (at % every.value == 0) {
           set_lds(p.to, i.value * 1024);
         } else if constexpr (at % every.value == 1) {
@@ -408,7 +416,9 @@ __global__ void __launch_bounds__(WM* WN* kWave)
     //   end  A's second half of k is read out, A's first and B of k + 1 have landed
     // The loads are A0 and B of k + 2 at the mid, A1 of k + 2 at the end: at either
     // sync all but the 2 AL + BL youngest have to have landed.
-    auto step = [&](auto compute, int k) {
+    // Only the first `live` row fragments are multiplied; 0: loads and syncs alone.
+    auto step = [&](auto live, int k) {
+      constexpr std::bool_constant<live.value == MF> whole{};
       Part p0, p1, p2;
       static_for<kGroups>([&](auto g) {
         if constexpr (g.value == kMid) {
@@ -420,30 +430,30 @@ __global__ void __launch_bounds__(WM* WN* kWave)
           sync_loads<2 * AL + BL>();
           p1 = part_of(i1, k + 2);
         }
-        if constexpr (compute.value) {
+        if constexpr (live.value > 0) {
           constexpr int kMidEvery = (kEnd - kMid) * NF / (AL + BL);
           constexpr int kEndEvery = kAhead * NF / AL;
           static_assert(kMidEvery >= 1 && kEndEvery >= 1, "a product for every load");
-          if constexpr (g.value + kAhead < kGroups) {
-            read_m(k, integral_constant<int, g.value + kAhead>{});
-          } else {
-            read_m(k + 1, integral_constant<int, g.value + kAhead - kGroups>{});
-          }
+          constexpr int ahead = (g.value + kAhead) % kGroups;
+          if constexpr (ahead / 2 < live.value)
+            read_m(g.value + kAhead < kGroups ? k : k + 1, integral_constant<int, ahead>{});
           static_for<NF>([&](auto u) {
             // a set of column fragments is read anew as soon as its last use is past
             if constexpr (g.value == 0) read_n(k, i1, u);
             if constexpr (g.value == kGroups - 1) read_n(k + 1, i0, u);
             if constexpr (g.value >= kMid && g.value < kEnd) {
               constexpr integral_constant<int, (g.value - kMid) * NF + u.value> slot{};
-              spread(i0, p0, slot, i0, integral_constant<int, kMidEvery>{});
-              spread(i2, p2, slot, integral_constant<int, AL>{},
-                     integral_constant<int, kMidEvery>{});
+              constexpr integral_constant<int, kMidEvery> every{};
+              spread(i0, p0, slot, i0, every, whole);
+              spread(i2, p2, slot, integral_constant<int, AL>{}, every, whole);
             }
             if constexpr (g.value >= kEnd) {
               constexpr integral_constant<int, (g.value - kEnd) * NF + u.value> slot{};
-              spread(i1, p1, slot, i0, integral_constant<int, kEndEvery>{});
+              spread(i1, p1, slot, i0, integral_constant<int, kEndEvery>{}, whole);
             }
-            mma<DT>(acc[g.value / 2][u.value], nf[g.value % 2][u.value], mf[g.value % 4]);
+            if constexpr (g.value / 2 < live.value) {
+              mma<DT>(acc[g.value / 2][u.value], nf[g.value % 2][u.value], mf[g.value % 4]);
+            }
             __builtin_amdgcn_sched_barrier(0);
           });
         } else if constexpr (g.value == kMid) {
@@ -454,26 +464,37 @@ __global__ void __launch_bounds__(WM* WN* kWave)
         }
       });
     };
-    auto all_steps = [&](auto compute) {
+    auto all_steps = [&](auto live) {
       static_for<2>([&](auto k) {
         load_part(i0, k);
         load_part(i2, k);
         load_part(i1, k);
       });
       sync_loads<2 * AL + BL>();
-      if constexpr (compute.value) {
+      if constexpr (live.value > 0) {
         static_for<NF>([&](auto f) { read_n(0, i0, f); });
         static_for<kAhead>([&](auto g) { read_m(0, g); });
       }
-      for (int k = 0; k < steps; ++k) step(compute, k);
+      for (int k = 0; k < steps; ++k) step(live, k);
       sync_loads<0>();  // no load is left in flight, and LDS is free again
     };
     const bool busy = wm * 16 < mrows && wn * (BN / WN) < ncols;
+    // Power bounds the large tile on ordinary operands, so one whose rows leave
+    // fragments empty (row segments end anywhere) leaves their products out, in
+    // steps of a quarter down to a half: with the rows shared out evenly, 256 rows
+    // an expert on average 306 -> 280 us (row gradient), a share of 32 experts
+    // of 1027 rows 1712 -> 1666.
+    constexpr bool kTrim = BM == 256 && P != kWeightGrad;
+    const int fragments = (mrows + 16 * WM - 1) / (16 * WM);
     if (steps > 0) {
-      if (busy) {
-        all_steps(std::true_type{});
+      if (!busy) {
+        all_steps(i0);
+      } else if (kTrim && fragments <= MF / 2) {
+        all_steps(integral_constant<int, kTrim ? MF / 2 : MF>{});
+      } else if (kTrim && fragments <= MF * 3 / 4) {
+        all_steps(integral_constant<int, kTrim ? MF * 3 / 4 : MF>{});
       } else {
-        all_steps(std::false_type{});
+        all_steps(integral_constant<int, MF>{});
       }
     }
     // a lane holds four consecutive columns of one row of each 16 x 16 block
