@@ -50,7 +50,7 @@ sys.path.insert(0, ROOT)
 HBM_PEAK_GBS = 8000.0          # MI355X HBM3E, 8 TB/s
 PROFILE_DIR = os.path.join(ROOT, "profiles")
 KERNEL_SOURCES = [os.path.join(ROOT, "combine_ep_prepare_amd", "csrc", f)
-                  for f in ("ep_kernels.hip", "ep_api.hip", "ep_internal.h")]
+                  for f in ("ep_kernels.hip", "ep_api.hip", "ep_internal.h", "ep_device.h")]
 
 STEP_OPS = ["prepare", "dispatch", "combine", "combine_bwd", "dispatch_bwd"]
 CEILINGS_LIB = os.path.join(ROOT, "combine_ep_prepare_amd", "libep_ceilings.so")
