@@ -32,7 +32,8 @@ live rows first; with ``fill_pads=False`` pad rows are unwritten too.
 `grouped_linear`, `swiglu` and `grouped_linear_quant` are the experts' own
 work between dispatch and combine: each expert's weights applied to its
 segment, and the gated activation. They read and write live rows only, so
-they give the same results with either policy.
+they give the same results with either policy. Their gradients are not
+differentiable again: a backward with ``create_graph=True`` is refused.
 """
 from __future__ import annotations
 
@@ -165,6 +166,13 @@ class _CombineWeighted(torch.autograd.Function):
         return grad_rows if want_rows else None, grad_w, None
 
 
+def _first_order_only(name: str):
+    # Grad mode is on in a backward only under create_graph; what the kernels
+    # write would stand in the new graph as a constant.
+    if torch.is_grad_enabled():
+        raise RuntimeError(f"{name} has no second derivative (create_graph=True)")
+
+
 class _GroupedLinear(torch.autograd.Function):
     @staticmethod
     def forward(ctx, x, weight, routing: EpRouting):
@@ -178,6 +186,7 @@ class _GroupedLinear(torch.autograd.Function):
 
     @staticmethod
     def backward(ctx, grad):
+        _first_order_only("grouped_linear")
         x, weight = ctx.saved_tensors
         L = ctx.routing.layout_for(x.dtype, x.shape[1])
         want_x, want_w = ctx.needs_input_grad[0], ctx.needs_input_grad[1]
@@ -202,6 +211,7 @@ class _SwiGLU(torch.autograd.Function):
 
     @staticmethod
     def backward(ctx, grad):
+        _first_order_only("swiglu")
         (gate_up,) = ctx.saved_tensors
         L = ctx.routing.layout_for(gate_up.dtype, gate_up.shape[1] // 2)
         grad_gate_up = torch.empty_like(gate_up)

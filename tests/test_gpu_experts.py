@@ -329,6 +329,25 @@ def test_special_values_reach_exactly_their_outputs(T):
     assert not torch.isfinite(gw[E - 1][:, bad]).any()
 
 
+@pytest.mark.parametrize("value", [float("inf"), float("nan"), 2.0 ** 127])
+@pytest.mark.parametrize("zeros", [False, True])
+def test_4_bit_special_values_stay_in_their_row(value, zeros):
+    H, N, E, G, T = 256, 72, 4, 64, 37
+    c = Case("one", T, 1, E, 8, "bf16", zero_tail=True)
+    x = c.buffer(H)
+    q, s, z, w = quantised(c, E, N, H, G, zeros)
+    s[:E - 1] = float("nan")                     # experts without rows
+    a = c.rows[E - 1][0]
+    clean, dirty = c.out(c.cap, N), c.out(c.cap, N)
+    args = [q.cuda(), s.cuda(), None if z is None else z.cuda()]
+    ep.grouped_linear_quant(c.layout(H), c.handle, x.cuda(), *args, clean)
+    x[a + 2, 5] = value
+    ep.grouped_linear_quant(c.layout(H), c.handle, x.cuda(), *args, dirty)
+    assert not torch.isfinite(dirty[a + 2].float()).any()
+    keep = torch.arange(c.cap, device="cuda") != a + 2
+    assert torch.isfinite(clean.float()).all() and torch.equal(clean[keep], dirty[keep])
+
+
 def test_foreign_layout_writes_nothing():
     c = Case("any", 40, 2, 4, 8, "bf16")
     H = N = 64
@@ -705,6 +724,17 @@ def test_expanded_and_strided_inputs():
     y2 = epa.swiglu(epa.grouped_linear(x2, w2, routing), routing)
     y2.backward(torch.ones_like(y2))
     assert torch.equal(y, y2) and torch.equal(x.grad, x2.grad) and torch.equal(wt.grad, w2.grad)
+
+
+def test_second_derivatives_are_refused():
+    T, K, E, H, I = 40, 2, 4, 64, 32
+    routing = epa.EpRouting(torch.from_numpy(route("any", T, K, E, 0)).cuda(), E, 4, H)
+    x = torch.randn(routing.layout.cap, H, device="cuda").requires_grad_()
+    w = torch.randn(E, 2 * I, H, device="cuda").requires_grad_()
+    y = epa.grouped_linear(x, w, routing)
+    for of, name in ((y, "grouped_linear"), (epa.swiglu(y, routing), "swiglu")):
+        with pytest.raises(RuntimeError, match=f"{name} has no second derivative"):
+            torch.autograd.grad(of.square().sum(), x, create_graph=True)
 
 
 def test_share_of_a_workload():
