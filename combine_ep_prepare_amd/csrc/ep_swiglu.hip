@@ -24,7 +24,8 @@ constexpr int kStepVectors = 8 * kThreads;
 
 // 1 / (1 + exp(-g)). The product with log2(e) is rounded, so exp(-g) is off by
 // |g| / 2 units in its last place at most besides the hardware's own one;
-// below g = -88 it is infinite and the result 0.
+// below g = -88 it is infinite and the result 0, and from -87.3 on the result
+// is subnormal, which the hardware's reciprocal may give as 0.
 __device__ __forceinline__ float sigmoid(float g) {
   return __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(g * -1.44269504088896340736f));
 }

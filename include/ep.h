@@ -429,7 +429,9 @@ ep_status_t ep_grouped_linear_bwd(const ep_layout_t* layout, const void* handle_
  * (decoding), right for any number. bf16 and fp16 payloads (fp32 is
  * EP_ERR_SHAPE); G is 32, 64 or 128 and divides H. The dequantised weight is
  * never rounded: q is an exact operand, and scale and zero point are applied
- * to each group's fp32 sum.
+ * to each group's fp32 sum. The operand is q plus an offset that leaves the
+ * group's sum again, so an x that is infinite, or in bf16 beyond 2^113, may
+ * reach its row of out as NaN; other rows are not touched by it.
  *   x             payload [recv_capacity,H], H = layout->hidden
  *   qweight       uint8 [E,N,H/2]; byte h/2 holds input h in its low four
  *                 bits for even h, in its high four bits for odd h
@@ -448,7 +450,8 @@ ep_status_t ep_grouped_linear_quant(const ep_layout_t* layout, const void* handl
 
 /*
  * Gated activation: out[r,i] = silu(gate_up[r,i]) * gate_up[r,I+i] for every
- * live row r, silu(g) = g / (1 + exp(-g)), I = layout->hidden.
+ * live row r, silu(g) = g / (1 + exp(-g)), I = layout->hidden. Computed in
+ * fp32 up to the one rounding; 1 / (1 + exp(-g)) may be 0 for g below -87.
  *   gate_up  payload [recv_capacity,2I]
  *   out      payload [recv_capacity,I]
  */
