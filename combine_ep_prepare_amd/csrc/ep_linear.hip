@@ -176,19 +176,27 @@ struct Operand {
   }
 };
 
-// Four results of a row, rounded and stored.
+// Four results rounded to 16 bits.
 template <int DT>
-__device__ __forceinline__ void store4(void* p, int64_t i, f32x4 v) {
-  if constexpr (DT == EP_DTYPE_FP32) {
-    *reinterpret_cast<row16_t*>(static_cast<float*>(p) + i) =
-        row16_t{canon_f32(v[0]), canon_f32(v[1]), canon_f32(v[2]), canon_f32(v[3])};
-  } else if constexpr (DT == EP_DTYPE_BF16) {
-    *reinterpret_cast<u32x2*>(static_cast<uint16_t*>(p) + i) = u32x2{
-        rne_bf16(v[0]) | (rne_bf16(v[1]) << 16), rne_bf16(v[2]) | (rne_bf16(v[3]) << 16)};
+__device__ __forceinline__ u32x2 round4(f32x4 v) {
+  if constexpr (DT == EP_DTYPE_BF16) {
+    return u32x2{rne_bf16(v[0]) | (rne_bf16(v[1]) << 16),
+                 rne_bf16(v[2]) | (rne_bf16(v[3]) << 16)};
   } else {
-    *reinterpret_cast<u32x2*>(static_cast<uint16_t*>(p) + i) = u32x2{
-        rne_f16(v[0]) | (rne_f16(v[1]) << 16), rne_f16(v[2]) | (rne_f16(v[3]) << 16)};
+    return u32x2{rne_f16(v[0]) | (rne_f16(v[1]) << 16), rne_f16(v[2]) | (rne_f16(v[3]) << 16)};
   }
+}
+
+// A lane of quarter q holds columns 4 q to 4 q + 3 of two neighbouring blocks
+// of 16, and gets columns 8 q to 8 q + 7 of the 32: stores of 16 bytes, 64 to a
+// row, in place of 8 and 32. Lanes trade with their like of the other quarters,
+// which hold the same row.
+__device__ __forceinline__ row16_t join_blocks(u32x2 a, u32x2 b) {
+  const auto lo = __builtin_amdgcn_permlane32_swap(a[0], b[0], false, false);
+  const auto hi = __builtin_amdgcn_permlane32_swap(a[1], b[1], false, false);
+  const auto l = __builtin_amdgcn_permlane16_swap(lo[0], lo[1], false, false);
+  const auto h = __builtin_amdgcn_permlane16_swap(hi[0], hi[1], false, false);
+  return row16_t{l[0], h[0], l[1], h[1]};
 }
 
 // Row tiles of an expert whose column tiles run together: with the columns
@@ -501,11 +509,21 @@ __global__ void __launch_bounds__(WM* WN* kWave)
     if (busy) {
       static_for<MF>([&](auto i) {
         const int32_t m = (i * WM + wm) * 16 + (lane & 15);
-        if (m < mrows) {
-          const int64_t r = P == kWeightGrad ? (int64_t)e * N + m0 + m : s.row + m0 + m;
+        const int64_t r = P == kWeightGrad ? (int64_t)e * N + m0 + m : s.row + m0 + m;
+        char* to = static_cast<char*>(c) + (r * cols + n0) * kSize;
+        if constexpr (DT == EP_DTYPE_FP32) {
           static_for<NF>([&](auto j) {
             const int32_t n = wn * (BN / WN) + j * 16 + (lane >> 4) * 4;
-            if (n < ncols) store4<DT>(c, r * cols + n0 + n, acc[i][j]);
+            const f32x4 v = acc[i][j];
+            if (m < mrows && n < ncols)
+              *reinterpret_cast<row16_t*>(to + n * kSize) =
+                  row16_t{canon_f32(v[0]), canon_f32(v[1]), canon_f32(v[2]), canon_f32(v[3])};
+          });
+        } else {
+          static_for<NF / 2>([&](auto j) {
+            const row16_t v = join_blocks(round4<DT>(acc[i][2 * j]), round4<DT>(acc[i][2 * j + 1]));
+            const int32_t n = wn * (BN / WN) + j * 32 + (lane >> 4) * 8;
+            if (m < mrows && n < ncols) *reinterpret_cast<row16_t*>(to + n * kSize) = v;
           });
         }
       });
