@@ -220,7 +220,7 @@ constexpr int kChunk = 32;
 // cover the other's LDS reads and barriers; four with twice the columns each
 // read a third less from LDS but ran at 1162.
 // ONCE: B is expected to be read by one tile alone (a single row tile an
-// expert) and passes by the caches.
+// expert) and passes by the caches; in the weight gradient, C does.
 template <int DT, int P, int BM, int BN, int WM, int WN, bool ONCE>
 __global__ void __launch_bounds__(WM* WN* kWave)
     grouped_product_kernel(Dims d, HandleView hv, const void* __restrict__ a,
@@ -231,6 +231,7 @@ __global__ void __launch_bounds__(WM* WN* kWave)
   constexpr int kWaves = WM * WN, kThreads = kWaves * kWave;
   constexpr int MF = BM / WM / 16, NF = BN / WN / 16;
   constexpr int kStage = 2 * A::kBytes + B::kBytes;
+  constexpr bool kOnceB = ONCE && P != kWeightGrad, kOnceC = ONCE && P == kWeightGrad;
   constexpr int AL = A::kLoads / kWaves, BL = B::kLoads / kWaves;
   static_assert(AL * kWaves == A::kLoads && BL * kWaves == B::kLoads, "whole loads");
   extern __shared__ __align__(1024) char lds[];
@@ -362,13 +363,13 @@ __global__ void __launch_bounds__(WM* WN* kWave)
       return p;
     };
     auto load_at = [&](auto part, const Part& p, auto i) {   // m0 is set
-      load_lds<(part.value == 2 && ONCE)>(
+      load_lds<(part.value == 2 && kOnceB)>(
           p.buffer, part.value == 2 ? b_off[i.value] : a_off[part.value & 1][i.value]);
     };
     auto load_part = [&](auto part, int k) {
       const Part p = part_of(part, k);
       static_for<part.value == 2 ? BL : AL>([&](auto i) {
-        load_to_lds<(part.value == 2 && ONCE)>(
+        load_to_lds<(part.value == 2 && kOnceB)>(
             p.buffer, part.value == 2 ? b_off[i.value] : a_off[part.value & 1][i.value],
             p.to + i.value * 1024);
       });
@@ -407,7 +408,7 @@ __global__ void __launch_bounds__(WM* WN* kWave)
         constexpr integral_constant<int, at / every.value> i{};
         if constexpr (every.value == 1 || !whole.value) {
           if constexpr (at % every.value == 0) {
-            load_to_lds<(part.value == 2 && ONCE)>(
+            load_to_lds<(part.value == 2 && kOnceB)>(
                 p.buffer, part.value == 2 ? b_off[i.value] : a_off[part.value & 1][i.value],
                 p.to + i.value * 1024);
           }
@@ -523,7 +524,14 @@ __global__ void __launch_bounds__(WM* WN* kWave)
           static_for<NF / 2>([&](auto j) {
             const row16_t v = join_blocks(round4<DT>(acc[i][2 * j]), round4<DT>(acc[i][2 * j + 1]));
             const int32_t n = wn * (BN / WN) + j * 32 + (lane >> 4) * 8;
-            if (m < mrows && n < ncols) *reinterpret_cast<row16_t*>(to + n * kSize) = v;
+            if (m < mrows && n < ncols) {
+              row16_t* at = reinterpret_cast<row16_t*>(to + n * kSize);
+              if constexpr (kOnceC) {
+                store_stream16(at, v);
+              } else {
+                *at = v;
+              }
+            }
           });
         }
       });
@@ -578,8 +586,16 @@ hipError_t launch_product(const Dims& d, const HandleView& hv, const void* a, co
       // 256 x 256 tiles from 129 rows, if they fill the CUs: 192 rows 240 us
       // against 272, 128 rows 300 against 238
       const int64_t tiles = (rows + 255) / 256 * ((cols + 255) / 256) * d.E;
-      if (rows > 128 && cols > 128 && tiles >= num_cus)
+      if (rows > 128 && cols > 128 && tiles >= num_cus) {
+        // weight gradients are stored past the caches up to 768 rows an expert,
+        // where their bytes count more than the products: 1 row 192 us against
+        // 204, 256 rows 370 against 400, 768 rows 660 against 672, but 1027 rows
+        // (7168 inputs, 4096 outputs) 1828 against 1820 and 4096 2970 against 2918
+        if (P == kWeightGrad && d.T * d.K / d.E <= 768)
+          return launch_tiles<DT, P, 256, 256, 2, 4, P == kWeightGrad>(d, hv, a, b, c, N, num_cus,
+                                                                       1, stream);
         return launch_tiles<DT, P, 256, 256, 2, 4>(d, hv, a, b, c, N, num_cus, 1, stream);
+      }
     }
     // 64 x 64 tiles where larger ones would leave CUs without work (one expert of
     // 256 rows, 4096 x 4096: 27 us against 44; fp32's weight gradient of five of

@@ -135,6 +135,8 @@ SHAPES = [
     ("masked", 1300, 2, 64, 8, 520, 648),
     ("any", 8400, 2, 112, 1, 520, 520),
     ("steep", 9000, 2, 112, 4, 520, 776),
+    # many rows an expert
+    ("any", 3250, 4, 16, 8, 1032, 1048),
 ]
 IDS = [f"{s[0]}-T{s[1]}E{s[3]}H{s[5]}N{s[6]}" for s in SHAPES]
 
