@@ -451,7 +451,9 @@ ep_status_t ep_grouped_linear_quant(const ep_layout_t* layout, const void* handl
 /*
  * Gated activation: out[r,i] = silu(gate_up[r,i]) * gate_up[r,I+i] for every
  * live row r, silu(g) = g / (1 + exp(-g)), I = layout->hidden. Computed in
- * fp32 up to the one rounding; 1 / (1 + exp(-g)) may be 0 for g below -87.
+ * fp32 up to the one rounding, for fp32 payloads with errors of the last bits
+ * whatever the gate. 1 / (1 + exp(-g)) counts also where it is below fp32's
+ * range; for g below -174, where it is under 2^-251, it may be 0.
  *   gate_up  payload [recv_capacity,2I]
  *   out      payload [recv_capacity,I]
  */
