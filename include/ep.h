@@ -428,10 +428,11 @@ ep_status_t ep_grouped_linear_bwd(const ep_layout_t* layout, const void* handle_
  * q in 0..15, G = group_size inputs to a group. Built for few rows per expert
  * (decoding), right for any number. bf16 and fp16 payloads (fp32 is
  * EP_ERR_SHAPE); G is 32, 64 or 128 and divides H. The dequantised weight is
- * never rounded: q is an exact operand, and scale and zero point are applied
- * to each group's fp32 sum. The operand is q plus an offset that leaves the
- * group's sum again, so an x that is infinite, or in bf16 beyond 2^113, may
- * reach its row of out as NaN; other rows are not touched by it.
+ * never rounded: scale and zero point act on fp32 sums over a group. For fp16
+ * these are sums of (q - z) x, of exact operands. For bf16 they are sums of
+ * (16 + q) x that start at -(16 + z) times the sum of x, so an x that is
+ * infinite, or beyond 2^112, may reach its row of out as NaN; other rows are not
+ * touched by it.
  *   x             payload [recv_capacity,H], H = layout->hidden
  *   qweight       uint8 [E,N,H/2]; byte h/2 holds input h in its low four
  *                 bits for even h, in its high four bits for odd h

@@ -88,3 +88,109 @@ def test_bf16_activation_of_gates_below_minus_87(up_scale):
         assert over.max() <= 0, (name, int((over > 0).sum()), float(over.max()))
         if name != "d_up" and up_scale > 1:
             assert (got != 0).float().mean() > 0.9
+
+
+# --------------------------------------------------------------------------
+# 4-bit weights
+# --------------------------------------------------------------------------
+
+def packed(q):
+    return q[..., 0::2] | (q[..., 1::2] << 4)
+
+
+def quant(c, x, q, scales, zeros):
+    E, N, H = q.shape
+    out = c.out(c.cap, N)
+    ep.grouped_linear_quant(c.layout(H), c.handle, x.cuda(), packed(q).cuda(), scales.cuda(),
+                            None if zeros is None else zeros.cuda(), out)
+    return out.double().cpu()
+
+
+def quant64(c, x, q, scales, zeros, G):
+    """The definition, and the magnitudes (q - z) x s that it adds up."""
+    E, N, H = q.shape
+    z = torch.full(scales.shape, 8.0) if zeros is None else zeros
+    w = (q.double().reshape(E, N, -1, G) - z.double()[..., None]) * scales.double()[..., None]
+    w = w.reshape(E, N, H)
+    want, mags = (torch.zeros(c.cap, N, dtype=torch.float64) for _ in range(2))
+    for e, (a, b) in enumerate(c.rows):
+        want[a:b] = x[a:b].double() @ w[e].t()
+        mags[a:b] = x[a:b].double().abs() @ w[e].abs().t()
+    return want, mags
+
+
+@pytest.mark.parametrize("zeros", [False, True])
+@pytest.mark.parametrize("G", [32, 64, 128])
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+def test_4_bit_weights_near_their_zero_point(dtype, G, zeros):
+    """One weight in sixteen differs from its zero point, by one, and x is
+    positive: the sums of q x and of z x are hundreds of times the result."""
+    T, E, N, H = 19, 2, 72, 640
+    c = Case("one", T, 1, E, 1, dtype)
+    g = c.gen
+    # 8 bits over four powers of two, steps of 2^-7; the inputs that count in [1, 2)
+    x = (1 + torch.randint(0, 128, (c.cap, H), generator=g) / 128) * \
+        2.0 ** torch.randint(0, 4, (c.cap, H), generator=g)
+    x[:, ::16] = 1 + torch.randint(0, 128, (c.cap, H // 16), generator=g) / 128
+    x = x.to(c.dtype)
+    x[~c.live] = float("nan")
+    z = torch.randint(1, 15, (E, N, H // G), generator=g, dtype=torch.uint8) if zeros else None
+    q = torch.full((E, N, H), 8, dtype=torch.uint8) if z is None else \
+        z.repeat_interleave(G, 2).clone()
+    q[..., ::16] += torch.randint(0, 3, (E, N, H // 16), generator=g, dtype=torch.uint8) - 1
+    s = (torch.rand(E, N, H // G, generator=g) * 0.01 + 1e-3).to(c.dtype)
+    got = quant(c, x, q, s, z)
+    want, mags = quant64(c, x, q, s, z, G)
+    # a group's sums are exact: of whole multiples of 2^-7, up to 31 * 16 * 128 =
+    # 2^15.9 in size, 23 bits. The scales and the sum over groups and wavefronts
+    # round: at most two steps a group and eight more.
+    bound = (2 * (H // G) + 8) * 2.0 ** -23 * mags
+    tol = bound + c.eps2 * (want.abs() + bound) + c.tiny
+    over = ((got - want).abs() - tol)[c.live]
+    assert over.max() <= 0, (int((over > 0).sum()), float(over.max()))
+
+
+@pytest.mark.parametrize("G", [32, 64, 128])
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+@pytest.mark.parametrize("T", [3, 700])
+def test_4_bit_zero_points_of_any_byte(T, dtype, G):
+    """Zero points from 0 to 255, and rows with a mean; few rows an expert and
+    many."""
+    E, N, H = 3, 136, 384
+    c = Case("steep", T, 1, E, 4, dtype, zero_tail=True)
+    x = c.buffer(H) + 2
+    q = torch.randint(0, 16, (E, N, H), generator=c.gen, dtype=torch.uint8)
+    z = torch.randint(0, 256, (E, N, H // G), generator=c.gen, dtype=torch.uint8)
+    z[0, 0], z[0, 1] = 0, 255
+    s = (torch.rand(E, N, H // G, generator=c.gen) * 1e-3 + 1e-4).to(c.dtype)
+    got = quant(c, x, q, s, z)
+    want, mags = quant64(c, x, q, s, z, G)
+    # fp16: the definition's own sums; bf16: those of (16 + q) x and (16 + z) x
+    bound = (H + 8) * 2.0 ** -23 * mags
+    if dtype == "bf16":
+        for e, (a, b) in enumerate(c.rows):
+            terms = (32.0 + 15 + z[e].double()) * s[e].double()
+            bound[a:b] += (G + 8) * 2.0 ** -23 * (x[a:b].double().abs()
+                                                  @ terms.repeat_interleave(G, 1).t())
+    tol = bound + c.eps2 * (want.abs() + bound) + c.tiny
+    over = ((got - want).abs() - tol)[c.live]
+    assert over.max() <= 0, (int((over > 0).sum()), float(over.max()))
+
+
+@pytest.mark.parametrize("value", [float("inf"), -float("inf"), float("nan"), 65504.0])
+@pytest.mark.parametrize("zeros", [False, True])
+def test_4_bit_fp16_special_values_follow_the_definition(value, zeros):
+    T, E, N, H, G = 21, 2, 40, 256, 64
+    c = Case("one", T, 1, E, 1, "fp16")
+    x = c.buffer(H)
+    q = torch.randint(0, 16, (E, N, H), generator=c.gen, dtype=torch.uint8)
+    z = torch.randint(0, 16, (E, N, H // G), generator=c.gen, dtype=torch.uint8) if zeros else None
+    s = torch.full((E, N, H // G), 0.5 ** 10, dtype=torch.float16)
+    r = c.rows[E - 1][0] + 5
+    x[r, 70] = value
+    got = quant(c, x, q, s, z)
+    want, _ = quant64(c, x, q, s, z, G)
+    assert torch.equal(got[c.live].isnan(), want[c.live].isnan())
+    assert torch.equal(got[c.live].isinf(), want[c.live].isinf())
+    inf = want.isinf() & c.live[:, None]
+    assert torch.equal(got[inf], want[inf])
