@@ -155,8 +155,10 @@ struct Stream {
 
   row16_t w[kLoads];
   row16_t x[kParts];                   // of the half that comes next
-  uint16_t scale[QUANT ? kRows : 1];   // of column `lane`
-  uint8_t zero[QUANT ? kRows : 1];
+  // of column `lane`, as they lie in memory: a register holds two scales or
+  // four zero points until the step's end
+  uint32_t scale[QUANT ? kRows / 2 : 1];
+  uint32_t zero[QUANT ? (kRows + 3) / 4 : 1];
 
   __device__ static __forceinline__ int32_t input(int half, int t) {
     const int q = lane_id() >> 4;
@@ -184,14 +186,17 @@ struct Stream {
       const int32_t all = H / G, g0 = k0 / G;
       const int64_t row = (int64_t)(lane < s.cols ? lane : 0) * all + g0;
       if constexpr (PART) {
+        static_for<kRows / 2>([&](auto g) { scale[g] = 0; });
+        static_for<(kRows + 3) / 4>([&](auto g) { zero[g] = 0; });
         static_for<kRows>([&](auto g) {
           const bool have = g0 + g < all;
-          scale[g] = have ? s.scales[row + g] : 0;
-          if constexpr (ZEROS) zero[g] = have ? s.zeros[row + g] : 0;
+          if (have) scale[g / 2] |= (uint32_t)s.scales[row + g] << (g % 2 * 16);
+          if constexpr (ZEROS)
+            if (have) zero[g / 4] |= (uint32_t)s.zeros[row + g] << (g % 4 * 8);
         });
       } else {
-        __builtin_memcpy(scale, s.scales + row, sizeof(scale));
-        if constexpr (ZEROS) __builtin_memcpy(zero, s.zeros + row, sizeof(zero));
+        __builtin_memcpy(scale, s.scales + row, kRows * 2);
+        if constexpr (ZEROS) __builtin_memcpy(zero, s.zeros + row, kRows);
       }
     }
   }
@@ -218,12 +223,14 @@ struct Stream {
       float* scales = reinterpret_cast<float*>(lds + kCols * 128);
       float* zeros = scales + kRows * kLdsRow;
       static_for<kRows>([&](auto g) {
-        scales[g * kLdsRow + lane] = DT == EP_DTYPE_BF16
-                                         ? __uint_as_float((uint32_t)scale[g] << 16)
-                                         : f16_to_f32(scale[g]);
-        if constexpr (ZEROS)
-          zeros[g * kLdsRow + lane] = kExact ? __uint_as_float(minus_zero(zero[g]))
-                                             : -(Offset<DT>::kValue + (float)zero[g]);
+        const uint32_t sc = g % 2 ? scale[g / 2] >> 16 : scale[g / 2] & 0xFFFFu;
+        scales[g * kLdsRow + lane] =
+            DT == EP_DTYPE_BF16 ? __uint_as_float(sc << 16) : f16_to_f32(sc);
+        if constexpr (ZEROS) {
+          const uint32_t z = (zero[g / 4] >> (g % 4 * 8)) & 0xFFu;
+          zeros[g * kLdsRow + lane] = kExact ? __uint_as_float(minus_zero(z))
+                                             : -(Offset<DT>::kValue + (float)z);
+        }
       });
     }
     __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
@@ -313,9 +320,12 @@ struct Stream {
   }
 };
 
-// Blocks (of one wavefront a SIMD) to a CU: as many as the registers hold. The
-// 4-bit form in the 128 registers that four leave spills, at twice the time;
-// 16-bit weights with four against three ran 90 against 95 us (sixteen
+// Blocks (of one wavefront a SIMD) to a CU, by the registers that they leave a
+// wavefront. The 4-bit form in the 128 of four spills, at twice the time. Three
+// leave 168, which hold all of its instances but the bf16 one with groups of 32
+// and zero points: that one keeps 6 registers in scratch, and ran 45.6 us against
+// 49.1 with two blocks and none there (16 rows, 128 experts, 2048 inputs, 1536
+// outputs). 16-bit weights with four against three ran 90 against 95 us (sixteen
 // tokens, top-8 of 128).
 constexpr int blocks_per_cu(bool quant) { return quant ? 3 : 4; }
 
@@ -353,7 +363,8 @@ __global__ void __launch_bounds__(kThreads, blocks_per_cu(QUANT))
     int32_t rows;
   };
   auto place = [&](int64_t t) {
-    // the row tiles of an expert are neighbours: they share their weights
+    // the row tiles of an expert are neighbours: they run at the same time, and
+    // each reads the weights for itself
     const int e = __builtin_amdgcn_readfirstlane(
         expert_of_tile(tile_start, d.E, (int32_t)(t / ct)));
     const int64_t in_e = t - tile_start[e] * ct;
