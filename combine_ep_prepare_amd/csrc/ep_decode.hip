@@ -27,6 +27,7 @@
 //   (batch of 32, 256 experts: 453 us against 445).
 // The scale is applied to the group's fp32 sum; no weight is rounded.
 
+#include "ep_choice.h"
 #include "ep_experts.h"
 
 namespace epmi {
@@ -448,7 +449,7 @@ hipError_t launch_few_rows(const Dims& d, const HandleView& hv, const void* x, c
                            const void* scales, const uint8_t* zeros, void* out, int64_t N,
                            int num_cus, hipStream_t stream) {
   const int64_t ct = (N + kCols - 1) / kCols;
-  const int64_t routes = d.T * d.K < d.cap ? d.T * d.K : d.cap;
+  const int64_t routes = most_rows(d);
   int64_t blocks = (routes / kRowTile + (d.E < routes ? d.E : routes)) * ct;
   const int64_t most = (int64_t)num_cus * blocks_per_cu(QUANT);
   if (blocks > most) blocks = most;

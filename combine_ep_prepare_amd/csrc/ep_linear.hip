@@ -10,13 +10,12 @@
 // is its contiguous axis (x and W forward, g in dgrad), else MN-major (W in
 // dgrad, both operands in wgrad).
 
+#include "ep_choice.h"
 #include "ep_experts.h"
 
 namespace epmi {
 
 namespace {
-
-enum Product { kForward, kRowGrad, kWeightGrad };
 
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
@@ -549,9 +548,9 @@ hipError_t launch_tiles(const Dims& d, const HandleView& hv, const void* a, cons
   auto* kernel = grouped_product_kernel<DT, P, BM, BN, WM, WN, ONCE>;
   const int64_t cols = P == kForward ? N : d.H;
   const int64_t ct = (cols + BN - 1) / BN;
-  // the most row tiles that the routing may need: every route's row, and one
-  // part tile an expert
-  const int64_t routes = d.T * d.K < d.cap ? d.T * d.K : d.cap;
+  // the most row tiles that the routing may need: those of all rows, and one part
+  // tile an expert
+  const int64_t routes = most_rows(d);
   int64_t blocks;
   if (P == kWeightGrad) {
     blocks = (int64_t)d.E * ((N + BM - 1) / BM) * ct;
@@ -572,47 +571,27 @@ hipError_t launch_tiles(const Dims& d, const HandleView& hv, const void* a, cons
 template <int P>
 hipError_t launch_product(const Dims& d, const HandleView& hv, const void* a, const void* b,
                           void* c, int64_t N, int num_cus, hipStream_t stream) {
+  const Kernel kernel = kernel_of((Product)P, d, N, num_cus);
   return with_payload(d.dtype, [&](auto dt) {
     constexpr int DT = decltype(dt)::value;
-    // Rows per expert, were the routes spread evenly; measured at 128 experts,
-    // 2048 inputs and 1536 outputs in bf16.
-    const int64_t rows = P == kWeightGrad ? N : d.T * d.K / d.E;
-    const int64_t cols = P == kForward ? N : d.H;
+    constexpr bool kWeights = P == kWeightGrad;
     if constexpr (DT != EP_DTYPE_FP32) {
-      // up to 12 rows: 8 rows 135 us against 144 with the tiles below, one row 90
-      // against 103; 16 rows 193 against 152 (many experts then have more rows
-      // than the 16 of its pass)
-      if (P == kForward && rows <= 12)
-        return launch_grouped_few(d, hv, a, b, c, N, num_cus, stream);
-      // 256 x 256 tiles from 129 rows, if they fill the CUs: 192 rows 240 us
-      // against 272, 128 rows 300 against 238
-      const int64_t tiles = (rows + 255) / 256 * ((cols + 255) / 256) * d.E;
-      if (rows > 128 && cols > 128 && tiles >= num_cus) {
-        // weight gradients are stored past the caches up to 768 rows an expert,
-        // where their bytes count more than the products: 1 row 192 us against
-        // 204, 256 rows 370 against 400, 768 rows 660 against 672, but 1027 rows
-        // (7168 inputs, 4096 outputs) 1828 against 1820 and 4096 2970 against 2918
-        if (P == kWeightGrad && d.T * d.K / d.E <= 768)
-          return launch_tiles<DT, P, 256, 256, 2, 4, P == kWeightGrad>(d, hv, a, b, c, N, num_cus,
-                                                                       1, stream);
-        return launch_tiles<DT, P, 256, 256, 2, 4>(d, hv, a, b, c, N, num_cus, 1, stream);
+      switch (kernel) {
+        case Kernel::kFewRows:
+          return launch_grouped_few(d, hv, a, b, c, N, num_cus, stream);
+        case Kernel::kTile256:
+          return launch_tiles<DT, P, 256, 256, 2, 4>(d, hv, a, b, c, N, num_cus, 1, stream);
+        case Kernel::kTile256Once:
+          return launch_tiles<DT, P, 256, 256, 2, 4, kWeights>(d, hv, a, b, c, N, num_cus, 1,
+                                                               stream);
+        case Kernel::kTile128Once:
+          return launch_tiles<DT, P, 128, 128, 2, 2, !kWeights>(d, hv, a, b, c, N, num_cus, 2,
+                                                                stream);
+        default: break;
       }
     }
-    // 64 x 64 tiles where larger ones would leave CUs without work (one expert of
-    // 256 rows, 4096 x 4096: 27 us against 44; fp32's weight gradient of five of
-    // 6150 rows, 224 x 320: 121 against 413). fp32 is bound by its matrix
-    // instructions, not by loads, and gains up to four of the larger a CU.
-    const int64_t tiles = (rows + 127) / 128 * ((cols + 127) / 128) * d.E;
-    if (tiles < (DT == EP_DTYPE_FP32 ? 4 : 1) * num_cus)
+    if (kernel == Kernel::kTile64)
       return launch_tiles<DT, P, 64, 64, 2, 2>(d, hv, a, b, c, N, num_cus, 4, stream);
-    if constexpr (DT != EP_DTYPE_FP32) {
-      // weights past the caches up to 64 rows, where nearly all experts have one
-      // row tile: 16 rows 152 us against 166, 64 rows 175 against 180 (row
-      // gradient, 8 rows: 130 against 149); at 128 rows half of them have two
-      if (P != kWeightGrad && rows <= 64)
-        return launch_tiles<DT, P, 128, 128, 2, 2, P != kWeightGrad>(d, hv, a, b, c, N, num_cus,
-                                                                     2, stream);
-    }
     return launch_tiles<DT, P, 128, 128, 2, 2>(d, hv, a, b, c, N, num_cus, 2, stream);
   });
 }

@@ -388,6 +388,10 @@ ep_status_t ep_combine_weighted_bwd(const ep_layout_t* layout, const void* handl
  * in an order that is fixed for given sizes and routing (results are
  * bit-identical from run to run) and otherwise unspecified. An infinity or
  * NaN in an operand reaches exactly the outputs whose sums contain it.
+ * A product's kernel is chosen on the host for min(num_tokens * topk,
+ * recv_capacity) / num_experts rows an expert: where most routes are masked (a
+ * rank that holds a few of the experts), a capacity near the rows that can
+ * come serves few rows best, and one for every route costs up to a tenth.
  */
 #define EP_MAX_FEATURES (1 << 20)
 
