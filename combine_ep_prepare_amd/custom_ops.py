@@ -269,6 +269,37 @@ def _(grad, x, weight, handle, layout):
     return x.new_empty(x.shape), weight.new_empty(weight.shape)
 
 
+# The two gradients one by one, for a backward that is asked for one of them.
+
+@torch.library.custom_op(f"{NS}::grouped_linear_grad_x", mutates_args=())
+def grouped_linear_grad_x(grad: Tensor, weight: Tensor, handle: Tensor,
+                          layout: List[int]) -> Tensor:
+    """grad_x [cap,H] alone."""
+    gx = torch.empty(grad.shape[0], weight.shape[2], dtype=grad.dtype, device=grad.device)
+    _grouped_linear_bwd(_rows_layout(layout, weight.shape[2]), handle, grad, None, weight, gx,
+                        None)
+    return gx
+
+
+@grouped_linear_grad_x.register_fake
+def _(grad, weight, handle, layout):
+    return grad.new_empty((grad.shape[0], weight.shape[2]))
+
+
+@torch.library.custom_op(f"{NS}::grouped_linear_grad_weight", mutates_args=())
+def grouped_linear_grad_weight(grad: Tensor, x: Tensor, handle: Tensor,
+                               layout: List[int]) -> Tensor:
+    """grad_weight [E,N,H] alone."""
+    gw = torch.empty(layout[2], grad.shape[1], x.shape[1], dtype=grad.dtype, device=grad.device)
+    _grouped_linear_bwd(_rows_layout(layout, x.shape[1]), handle, grad, x, None, None, gw)
+    return gw
+
+
+@grouped_linear_grad_weight.register_fake
+def _(grad, x, handle, layout):
+    return grad.new_empty((layout[2], grad.shape[1], x.shape[1]))
+
+
 def _linear_setup(ctx, inputs, output):
     x, weight, handle, layout = inputs
     ctx.save_for_backward(x, weight, handle)
@@ -277,7 +308,14 @@ def _linear_setup(ctx, inputs, output):
 
 def _linear_backward(ctx, g):
     x, weight, handle = ctx.saved_tensors
-    gx, gw = grouped_linear_bwd(g.contiguous(), x, weight, handle, ctx.layout)
+    g, gx, gw = g.contiguous(), None, None
+    want_x, want_w = ctx.needs_input_grad[:2]
+    if want_x and want_w:
+        gx, gw = grouped_linear_bwd(g, x, weight, handle, ctx.layout)
+    elif want_x:
+        gx = grouped_linear_grad_x(g, weight, handle, ctx.layout)
+    elif want_w:
+        gw = grouped_linear_grad_weight(g, x, handle, ctx.layout)
     return gx, gw, None, None
 
 
