@@ -61,10 +61,11 @@ constexpr uint32_t kOutside = 0x40000000u;
 // 16 bytes per lane from a buffer straight into LDS: lane l's bytes land at
 // m0 + 16 l. Written out because the compiler makes every later LDS read wait
 // for such loads, also those of the other half of a double buffer; the wait
-// is in sync_stage below. Nothing else here lives in m0: the compiler sets it
-// right before each of its own uses. An instruction has to stand between the
-// write of m0 and the load: load_to_lds brings one, between set_lds and
-// load_lds the caller has a product.
+// is in sync_loads below. m0 is reserved in the compiler, so an asm statement
+// cannot tell it of a write: that nothing else in these kernels writes or reads
+// m0 is checked in their assembly (tests/test_experts_asm_m0.py). An instruction
+// has to stand between the write of m0 and the load: load_to_lds brings one,
+// between set_lds and load_lds the caller has a product.
 __device__ __forceinline__ void set_lds(uint32_t base, uint32_t offset) {
   asm volatile("s_add_u32 m0, %0, %1" ::"s"(base), "s"(offset) : "scc");
 }
