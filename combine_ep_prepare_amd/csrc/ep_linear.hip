@@ -273,6 +273,7 @@ __global__ void __launch_bounds__(WM* WN* kWave)
   const int64_t slots = P == kWeightGrad ? kChunk : gridDim.x / kRunXcds;
   const int64_t xcd = blockIdx.x % kRunXcds, slot = blockIdx.x / kRunXcds;
   int64_t t = ((slot / slots) * kRunXcds + xcd) * slots + slot % slots;
+  if constexpr (P == kWeightGrad) t += (int64_t)blockIdx.y * gridDim.x;
   for (; t < tiles; t += P == kWeightGrad ? tiles : (int64_t)gridDim.x) {
     // tile t: expert e, row tile mi, column tile ni
     int e;
@@ -563,9 +564,14 @@ hipError_t launch_tiles(const Dims& d, const HandleView& hv, const void* a, cons
   const int64_t unit = P == kWeightGrad ? kRunXcds * kChunk : kRunXcds;
   blocks = (blocks + unit - 1) / unit * unit;
   if (blocks < unit) blocks = unit;
-  if (blocks > 0x7FFFFF00) return hipErrorInvalidConfiguration;
+  // A grid has less than 2^32 threads in one direction: what is past them (2048
+  // experts of 8 x 2^20 weights) lies in the other.
+  const int64_t most = (int64_t)0xFFFFFFFF / (WM * WN * kWave) / unit * unit;
+  const int64_t deep = (blocks + most - 1) / most;
+  if (deep > 1) blocks = most;
   const size_t lds = 2 * (size_t)(BM + BN) * 128 + sizeof(int32_t) * (size_t)(d.E + 1 + 16);
-  kernel<<<dim3((uint32_t)blocks), dim3(WM * WN * kWave), lds, stream>>>(d, hv, a, b, c, N);
+  kernel<<<dim3((uint32_t)blocks, (uint32_t)deep), dim3(WM * WN * kWave), lds, stream>>>(
+      d, hv, a, b, c, N);
   return hipGetLastError();
 }
 
