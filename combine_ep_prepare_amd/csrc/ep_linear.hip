@@ -63,9 +63,11 @@ constexpr uint32_t kOutside = 0x40000000u;
 // for such loads, also those of the other half of a double buffer; the wait
 // is in sync_loads below. m0 is reserved in the compiler, so an asm statement
 // cannot tell it of a write: that nothing else in these kernels writes or reads
-// m0 is checked in their assembly (tests/test_experts_asm_m0.py). An instruction
-// has to stand between the write of m0 and the load: load_to_lds brings one,
-// between set_lds and load_lds the caller has a product.
+// m0 is checked in their assembly (tests/test_experts_asm_m0.py).
+// The load needs five wait states behind a vector instruction that wrote one of
+// the buffer's scalar registers (a register brought back from a lane, say, which
+// may come right before it), and one behind the write of m0. The compiler counts
+// neither for an asm statement, so each load brings them.
 __device__ __forceinline__ void set_lds(uint32_t base, uint32_t offset) {
   asm volatile("s_add_u32 m0, %0, %1" ::"s"(base), "s"(offset) : "scc");
 }
@@ -73,15 +75,15 @@ __device__ __forceinline__ void set_lds(uint32_t base, uint32_t offset) {
 template <bool ONCE>
 __device__ __forceinline__ void load_lds(row16_t buffer, uint32_t offset) {
   if constexpr (ONCE) {
-    asm volatile("buffer_load_dwordx4 %0, %1, 0 offen nt lds" ::"v"(offset), "s"(buffer)
+    asm volatile("s_nop 4\n\tbuffer_load_dwordx4 %0, %1, 0 offen nt lds" ::"v"(offset), "s"(buffer)
                  : "memory");
   } else {
-    asm volatile("buffer_load_dwordx4 %0, %1, 0 offen lds" ::"v"(offset), "s"(buffer) : "memory");
+    asm volatile("s_nop 4\n\tbuffer_load_dwordx4 %0, %1, 0 offen lds" ::"v"(offset), "s"(buffer) : "memory");
   }
 }
 template <bool ONCE>
 __device__ __forceinline__ void load_to_lds(row16_t buffer, uint32_t offset, uint32_t lds) {
-  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0" ::"s"(lds));
+  asm volatile("s_mov_b32 m0, %0" ::"s"(lds));
   load_lds<ONCE>(buffer, offset);
 }
 
