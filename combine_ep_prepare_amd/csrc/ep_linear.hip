@@ -59,32 +59,31 @@ __device__ __forceinline__ row16_t buffer_of(const void* p, uint32_t bytes) {
 constexpr uint32_t kOutside = 0x40000000u;
 
 // 16 bytes per lane from a buffer straight into LDS: lane l's bytes land at
-// m0 + 16 l. Written out because the compiler makes every later LDS read wait
-// for such loads, also those of the other half of a double buffer; the wait
-// is in sync_loads below. m0 is reserved in the compiler, so an asm statement
-// cannot tell it of a write: that nothing else in these kernels writes or reads
-// m0 is checked in their assembly (tests/test_experts_asm_m0.py).
+// lds + at + 16 l. Written out because the compiler makes every later LDS read wait
+// for such loads, also those of the other half of a double buffer; the wait is in
+// sync_loads below. The place goes through m0, which is reserved in the compiler
+// and which nothing else here uses.
 // The load needs five wait states behind a vector instruction that wrote one of
 // the buffer's scalar registers (a register brought back from a lane, say, which
 // may come right before it), and one behind the write of m0. The compiler counts
-// neither for an asm statement, so each load brings them.
-__device__ __forceinline__ void set_lds(uint32_t base, uint32_t offset) {
-  asm volatile("s_add_u32 m0, %0, %1" ::"s"(base), "s"(offset) : "scc");
-}
+// neither for an asm statement, so it holds both. They cost the large products
+// between 1 and 2% (backward of 8 experts of 4096 rows, 14336 x 4096: 6050 us without
+// and 6170 with them); two loads a statement, which share one wait, cost 3%.
 // ONCE: the bytes are read by one tile only and need not stay in the caches.
-template <bool ONCE>
-__device__ __forceinline__ void load_lds(row16_t buffer, uint32_t offset) {
-  if constexpr (ONCE) {
-    asm volatile("s_nop 4\n\tbuffer_load_dwordx4 %0, %1, 0 offen nt lds" ::"v"(offset), "s"(buffer)
-                 : "memory");
-  } else {
-    asm volatile("s_nop 4\n\tbuffer_load_dwordx4 %0, %1, 0 offen lds" ::"v"(offset), "s"(buffer) : "memory");
-  }
-}
-template <bool ONCE>
+template <bool ONCE, int AT>
 __device__ __forceinline__ void load_to_lds(row16_t buffer, uint32_t offset, uint32_t lds) {
-  asm volatile("s_mov_b32 m0, %0" ::"s"(lds));
-  load_lds<ONCE>(buffer, offset);
+  if constexpr (ONCE) {
+    asm volatile(
+        "s_add_u32 m0, %2, %3\n\ts_nop 3\n\tbuffer_load_dwordx4 %0, %1, 0 offen nt lds" ::"v"(
+            offset),
+        "s"(buffer), "s"(lds), "n"(AT)
+        : "memory", "scc");
+  } else {
+    asm volatile(
+        "s_add_u32 m0, %2, %3\n\ts_nop 3\n\tbuffer_load_dwordx4 %0, %1, 0 offen lds" ::"v"(offset),
+        "s"(buffer), "s"(lds), "n"(AT)
+        : "memory", "scc");
+  }
 }
 
 // For all wavefronts of the block: every LDS read is done, and every load
@@ -366,17 +365,13 @@ __global__ void __launch_bounds__(WM* WN* kWave)
                                             part.value * A::kBytes + wave * n * 1024);
       return p;
     };
-    auto load_at = [&](auto part, const Part& p, auto i) {   // m0 is set
-      load_lds<(part.value == 2 && kOnceB)>(
-          p.buffer, part.value == 2 ? b_off[i.value] : a_off[part.value & 1][i.value]);
+    auto load_at = [&](auto part, const Part& p, auto i) {
+      load_to_lds<(part.value == 2 && kOnceB), i.value * 1024>(
+          p.buffer, part.value == 2 ? b_off[i.value] : a_off[part.value & 1][i.value], p.to);
     };
     auto load_part = [&](auto part, int k) {
       const Part p = part_of(part, k);
-      static_for<part.value == 2 ? BL : AL>([&](auto i) {
-        load_to_lds<(part.value == 2 && kOnceB)>(
-            p.buffer, part.value == 2 ? b_off[i.value] : a_off[part.value & 1][i.value],
-            p.to + i.value * 1024);
-      });
+      static_for<part.value == 2 ? BL : AL>([&](auto i) { load_at(part, p, i); });
     };
 
     f32x4 acc[MF][NF];
@@ -402,26 +397,11 @@ __global__ void __launch_bounds__(WM* WN* kWave)
     constexpr integral_constant<int, 0> i0{};
     constexpr integral_constant<int, 1> i1{};
     constexpr integral_constant<int, 2> i2{};
-    // One load every EVERY products of a stretch: the first sets its place, the
-    // next one brings it. Without a product between the two (EVERY 1, or a tile
-    // that leaves some out) both come at once.
-    auto spread = [&](auto part, const Part& p, auto slot, auto first, auto every, auto whole) {
+    // One load every EVERY products of a stretch.
+    auto spread = [&](auto part, const Part& p, auto slot, auto first, auto every) {
       constexpr int at = slot.value - first.value * every.value;
-      constexpr int n = part.value == 2 ? BL : AL;
-      if constexpr (at >= 0 && at / every.value < n) {
-        constexpr integral_constant<int, at / every.value> i{};
-        if constexpr (every.value == 1 || !whole.value) {
-          if constexpr (at % every.value == 0) {
-            load_to_lds<(part.value == 2 && kOnceB)>(
-                p.buffer, part.value == 2 ? b_off[i.value] : a_off[part.value & 1][i.value],
-                p.to + i.value * 1024);
-          }
-        } else if constexpr (at % every.value == 0) {
-          set_lds(p.to, i.value * 1024);
-        } else if constexpr (at % every.value == 1) {
-          load_at(part, p, i);
-        }
-      }
+      if constexpr (at >= 0 && at % every.value == 0 && at / every.value < (part.value == 2 ? BL : AL))
+        load_at(part, p, integral_constant<int, at / every.value>{});
     };
     // Step k. Two syncs; what is read out at one makes room for loads that are
     // waited for a step and a half later:
@@ -431,7 +411,6 @@ __global__ void __launch_bounds__(WM* WN* kWave)
     // sync all but the 2 AL + BL youngest have to have landed.
     // Only the first `live` row fragments are multiplied; 0: loads and syncs alone.
     auto step = [&](auto live, int k) {
-      constexpr std::bool_constant<live.value == MF> whole{};
       Part p0, p1, p2;
       static_for<kGroups>([&](auto g) {
         if constexpr (g.value == kMid) {
@@ -457,12 +436,12 @@ __global__ void __launch_bounds__(WM* WN* kWave)
             if constexpr (g.value >= kMid && g.value < kEnd) {
               constexpr integral_constant<int, (g.value - kMid) * NF + u.value> slot{};
               constexpr integral_constant<int, kMidEvery> every{};
-              spread(i0, p0, slot, i0, every, whole);
-              spread(i2, p2, slot, integral_constant<int, AL>{}, every, whole);
+              spread(i0, p0, slot, i0, every);
+              spread(i2, p2, slot, integral_constant<int, AL>{}, every);
             }
             if constexpr (g.value >= kEnd) {
               constexpr integral_constant<int, (g.value - kEnd) * NF + u.value> slot{};
-              spread(i1, p1, slot, i0, integral_constant<int, kEndEvery>{}, whole);
+              spread(i1, p1, slot, i0, integral_constant<int, kEndEvery>{});
             }
             if constexpr (g.value / 2 < live.value) {
               mma<DT>(acc[g.value / 2][u.value], nf[g.value % 2][u.value], mf[g.value % 4]);

@@ -1,7 +1,7 @@
 """m0 in the gfx950 assembly of the grouped product (no GPU).
 
-Its loads into LDS take their place there from m0, which asm statements write a
-few instructions ahead. The compiler does not know of these writes. Checked here,
+Its loads into LDS take their place there from m0, which their asm statements
+write. The compiler does not know of these writes. Checked here,
 for every kernel built from the file: m0 appears in them and nowhere else, each
 load has its own write, and no branch target lies between the two.
 """
