@@ -10,6 +10,16 @@ namespace epmi {
 
 namespace {
 
+// Pieces of `size` that n is cut into, the last one perhaps a part.
+__host__ __device__ constexpr int32_t pieces(int32_t n, int32_t size) {
+  return n / size + (n % size != 0 ? 1 : 0);
+}
+
+// n - at, where `at` is at most a read-ahead past n: both may lie next to 2^31.
+__host__ __device__ constexpr int32_t rest_after(int32_t n, uint32_t at) {
+  return (int32_t)((uint32_t)n - at);
+}
+
 // The live rows of expert e: its valid routes' rows below the capacity. Pad
 // rows and rows dropped past the capacity are no operand of any product.
 struct Segment {
@@ -45,7 +55,7 @@ __device__ __forceinline__ int32_t list_tiles(const HandleView& hv, const Dims& 
   for (int e0 = 0; e0 < d.E; e0 += THREADS) {
     const int e = e0 + (int)threadIdx.x;
     const int32_t rows = e0 == 0 ? first_rows : e < d.E ? segment_of(hv, d, e).rows : 0;
-    const int32_t tiles = (rows + bm - 1) / bm;
+    const int32_t tiles = pieces(rows, bm);
     int32_t sum = tiles;
     static_for<6>([&](auto i) {
       const int32_t below = __shfl_up(sum, 1u << i, kWave);

@@ -320,7 +320,7 @@ __global__ void __launch_bounds__(WM* WN* kWave)
       a_src += (s.row + m0) * a_stride;
       b_src += (int64_t)e * N * b_stride + (P == kForward ? n0 * b_stride : n0 * kSize);
     }
-    const int steps = (depth + A::kDepth - 1) / A::kDepth;
+    const int32_t steps = pieces(depth, A::kDepth);
     uint32_t a_off[2][AL], b_off[BL];
     static_for<AL>([&](auto i) {
       static_for<2>([&](auto h) {
@@ -342,7 +342,8 @@ __global__ void __launch_bounds__(WM* WN* kWave)
       constexpr int n = kRows ? AL : BL;
       constexpr int kSkip = kRows ? part.value * (BM / 2) : 0;  // rows before the part
       uint32_t* off = kRows ? a_off[part.value & 1] : b_off;
-      const int32_t k0 = k * A::kDepth, left = depth - k0;
+      const uint32_t k0 = (uint32_t)k * A::kDepth;
+      const int32_t left = rest_after(depth, k0);
       const uint32_t stride = kRows ? a_stride : b_stride;
       const int32_t held = (kRows ? mrows : ncols) - kSkip;   // rows or columns of the part
       const char* src = kRows ? a_src : b_src;
@@ -353,7 +354,7 @@ __global__ void __launch_bounds__(WM* WN* kWave)
           const uint32_t out = A::chunk_k() < left ? 0 : kOutside;
           static_for<n>([&](auto i) { off[i] |= out; });
         }
-        const uint32_t byte0 = (uint32_t)k0 * kSize;
+        const uint32_t byte0 = k0 * kSize;
         p.buffer = buffer_of(src + (int64_t)kSkip * stride + byte0,
                              left > 0 && held > 0 ? (uint32_t)held * stride - byte0 : 0);
       } else {
