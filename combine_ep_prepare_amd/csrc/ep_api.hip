@@ -386,7 +386,7 @@ ep_status_t ep_grouped_linear_bwd(const ep_layout_t* layout, const void* handle_
   if (st != EP_OK) return st;
   if (!features_ok(d.H) || !features_ok(out_features)) return EP_ERR_SHAPE;
   if (d.cap > 0 && !grad) return EP_ERR_NULL;
-  if (!grad_x && !grad_weight) return EP_ERR_NULL;
+  if (d.cap > 0 && !grad_x && !grad_weight) return EP_ERR_NULL;
   if (grad_x && !weight) return EP_ERR_NULL;
   if (grad_weight && d.cap > 0 && !x) return EP_ERR_NULL;
   if (!aligned16(grad) || !aligned16(x) || !aligned16(weight) || !aligned16(grad_x) ||

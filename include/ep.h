@@ -414,7 +414,8 @@ ep_status_t ep_grouped_linear(const ep_layout_t* layout, const void* handle_mem,
  *   grad_weight[e,n,:]  = sum over the live rows r of e of grad[r,n] * x[r,:]
  * grad_weight is written whole: an expert without a live row gets +0. Either
  * output may be NULL and is then skipped, together with the operand only it
- * needs (weight for grad_x, x for grad_weight); both NULL is EP_ERR_NULL.
+ * needs (weight for grad_x, x for grad_weight); both NULL is EP_ERR_NULL, but
+ * with recv_capacity 0, where a grad_x of no rows may be NULL.
  *   grad         payload [recv_capacity,N]
  *   x            payload [recv_capacity,H] or NULL
  *   weight       payload [E,N,H] or NULL
