@@ -31,7 +31,7 @@ inline int64_t most_rows(const Dims& d) {
 // bf16 at 128 experts, 2048 inputs and 1536 outputs, no route masked, the capacity
 // no less than the routes, unless another size is named; a rank's 32 of 256
 // experts (7168 inputs, 4096 outputs, a capacity a quarter above its rows) has its
-// borders at the same rows.
+// borders at about the same rows.
 inline Kernel kernel_of(Product p, const Dims& d, int64_t N, int num_cus) {
   const bool bits16 = d.dtype != EP_DTYPE_FP32;
   const int64_t per_expert = most_rows(d) / d.E;

@@ -325,9 +325,9 @@ struct Stream {
 // wavefront. The 4-bit form in the 128 of four spills, at twice the time. Three
 // leave 168, which hold all of its instances but the bf16 one with groups of 32
 // and zero points: that one keeps 6 registers in scratch, and ran 45.6 us against
-// 49.1 with two blocks and none there (16 rows, 128 experts, 2048 inputs, 1536
-// outputs). 16-bit weights with four against three ran 90 against 95 us (sixteen
-// tokens, top-8 of 128).
+// 49.1 with two blocks and none there (sixteen tokens, top-8 of 128, 2048 inputs,
+// 1536 outputs). 16-bit weights with four against three ran 90 against 95 us (the
+// same routing).
 constexpr int blocks_per_cu(bool quant) { return quant ? 3 : 4; }
 
 // Up to 16 rows of an expert by kCols columns a block step. The wavefronts

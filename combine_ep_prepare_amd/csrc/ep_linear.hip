@@ -401,7 +401,8 @@ __global__ void __launch_bounds__(WM* WN* kWave)
     // One load every EVERY products of a stretch.
     auto spread = [&](auto part, const Part& p, auto slot, auto first, auto every) {
       constexpr int at = slot.value - first.value * every.value;
-      if constexpr (at >= 0 && at % every.value == 0 && at / every.value < (part.value == 2 ? BL : AL))
+      constexpr int n = part.value == 2 ? BL : AL;
+      if constexpr (at >= 0 && at % every.value == 0 && at / every.value < n)
         load_at(part, p, integral_constant<int, at / every.value>{});
     };
     // Step k. Two syncs; what is read out at one makes room for loads that are
