@@ -229,9 +229,9 @@ def _run_own(s):
         ep.rms_norm_bwd(L, s["grad"], s["x"], s["weight"], EPS, out[0], out[1], s["workspace"],
                         grad_sum=s["grad_sum"])
     elif op == "linear":
-        ep.grouped_linear_fp8(L, s["handle"], s["x"], s["x_scales"], *s["w"], out[0])
+        ep.grouped_linear_scaled(L, s["handle"], s["x"], s["x_scales"], *s["w"], out[0])
     elif op == "act":
-        ep.swiglu_quant(L, s["handle"], s["gate_up"], out[0], out[1])
+        ep.swiglu_scaled(L, s["handle"], s["gate_up"], out[0], out[1])
     else:
         ep.expert_layer(L, s["idx"], s["w"], s["x"], s["gate_up"][0], s["down"][0], out, s["workspace"],
                         gate_up_scales=s["gate_up"][1], down_scales=s["down"][1])
