@@ -12,7 +12,8 @@ The five routing ops follow the per-step calls of "Expert Parallelism: common C 
 capturable)"): prepare, dispatch, combine, dispatch_bwd and combine_bwd. The
 experts' own work between dispatch and combine stands beside them: the grouped
 linear, its backward and its 4-bit form, and the gated activation with its
-backward.
+backward; the norm in front of a layer, and the linear and activation in 8 bits
+with scales; and the whole layer for a few tokens.
 """
 from __future__ import annotations
 
@@ -34,6 +35,7 @@ EP_ERR_CAPACITY = 5
 EP_ERR_DEVICE = 6
 EP_ERR_HIP = 7
 EP_ERR_SCRATCH = 8
+EP_ERR_WORKSPACE = 9
 PREPARE_STATIC_SCRATCH_BYTES = 4 << 20
 
 STATUS_BAD_EXPERT = 1
@@ -46,6 +48,11 @@ DTYPE_FP32 = 2
 LAYOUT_NO_PAD_FILL = 1
 LAYOUT_ZERO_TAIL = 4
 
+SCALE_BLOCK = 128          # values of a row to one scale, in 8 bits
+MAX_NORM_FEATURES = 16384
+MAX_LAYER_ROUTES = 1024
+E4M3 = torch.float8_e4m3fn  # the type of 8-bit values
+
 # payload type code -> torch dtype of the rows
 TORCH_DTYPE = {DTYPE_BF16: torch.bfloat16, DTYPE_FP16: torch.float16,
                DTYPE_FP32: torch.float32}
@@ -56,8 +63,10 @@ ENTRY_POINTS = ("ep_recv_capacity_worst", "ep_handle_mem_size", "ep_handle_regio
                 "ep_prepare", "ep_prepare_static", "ep_dispatch",
                 "ep_combine", "ep_dispatch_bwd", "ep_combine_bwd", "ep_combine_weighted",
                 "ep_combine_weighted_bwd", "ep_grouped_linear", "ep_grouped_linear_bwd",
-                "ep_grouped_linear_quant", "ep_swiglu", "ep_swiglu_bwd", "ep_read_status",
-                "ep_status_str")
+                "ep_grouped_linear_quant", "ep_swiglu", "ep_swiglu_bwd", "ep_rms_norm",
+                "ep_rms_norm_bwd", "ep_rms_norm_bwd_workspace", "ep_swiglu_scaled",
+                "ep_grouped_linear_scaled", "ep_expert_layer", "ep_expert_layer_workspace",
+                "ep_read_status", "ep_status_str")
 
 
 class Layout(C.Structure):
@@ -149,11 +158,22 @@ def _load_library(path: str = LIB_PATH):
     lib.ep_grouped_linear_quant.argtypes = [lp, vp, sz, vp, vp, vp, vp, vp, i64, i32, vp]
     lib.ep_swiglu.argtypes = [lp, vp, sz, vp, vp, vp]
     lib.ep_swiglu_bwd.argtypes = [lp, vp, sz, vp, vp, vp, vp]
+    lib.ep_rms_norm.argtypes = [lp, vp, vp, vp, C.c_float, vp, vp, vp, vp, vp]
+    lib.ep_rms_norm_bwd_workspace.argtypes = [lp]
+    lib.ep_rms_norm_bwd_workspace.restype = sz
+    lib.ep_rms_norm_bwd.argtypes = [lp, vp, vp, vp, vp, C.c_float, vp, vp, vp, sz, vp]
+    lib.ep_swiglu_scaled.argtypes = [lp, vp, sz, vp, vp, vp, vp]
+    lib.ep_grouped_linear_scaled.argtypes = [lp, vp, sz, vp, vp, vp, vp, vp, i64, vp]
+    lib.ep_expert_layer_workspace.argtypes = [lp, i64]
+    lib.ep_expert_layer_workspace.restype = sz
+    lib.ep_expert_layer.argtypes = [lp, vp, vp, vp, vp, vp, vp, vp, vp, i64, vp, sz, vp]
     for name in ("ep_prepare", "ep_prepare_static", "ep_dispatch", "ep_combine",
                  "ep_dispatch_bwd",
                  "ep_combine_bwd", "ep_combine_weighted", "ep_combine_weighted_bwd",
                  "ep_grouped_linear", "ep_grouped_linear_bwd", "ep_grouped_linear_quant",
-                 "ep_swiglu", "ep_swiglu_bwd", "ep_read_status"):
+                 "ep_swiglu", "ep_swiglu_bwd", "ep_rms_norm", "ep_rms_norm_bwd",
+                 "ep_swiglu_scaled", "ep_grouped_linear_scaled", "ep_expert_layer",
+                 "ep_read_status"):
         getattr(lib, name).restype = C.c_int
     lib.ep_status_str.argtypes = [C.c_int]
     lib.ep_status_str.restype = C.c_char_p
@@ -432,6 +452,139 @@ def swiglu_bwd(layout: Layout, handle: torch.Tensor, grad: torch.Tensor,
     _check(lib.ep_swiglu_bwd(C.byref(layout), _ptr(handle), handle.numel(), _ptr(grad),
                              _ptr(gate_up), _ptr(grad_gate_up), _stream(stream)),
            "ep_swiglu_bwd")
+
+
+def scale_columns(hidden: int) -> int:
+    """Scales that a row of ``hidden`` 8-bit values has room for."""
+    return (hidden + 1023) // 1024 * 8
+
+
+def _scale_blocks(n: int) -> int:
+    return (n + SCALE_BLOCK - 1) // SCALE_BLOCK
+
+
+def rms_norm(layout: Layout, x: torch.Tensor, weight: torch.Tensor, eps: float,
+             out: Optional[torch.Tensor] = None, out_q: Optional[torch.Tensor] = None,
+             out_scales: Optional[torch.Tensor] = None,
+             residual: Optional[torch.Tensor] = None,
+             sum_out: Optional[torch.Tensor] = None, stream=None):
+    """The norm of x [T,H] (with a residual: of sum_out = x + residual) times
+    weight [H], into out [T,H], or in 8 bits into out_q with out_scales
+    [T, scale_columns(H)], or both."""
+    rows, dtype = (layout.T, layout.H), layout.payload_dtype
+    _need(x, "x", dtype, rows)
+    _need(weight, "weight", dtype, (layout.H,))
+    _need(out, "out", dtype, rows, allow_none=out_q is not None)
+    _need(out_q, "out_q", E4M3, rows, allow_none=True)
+    _need(out_scales, "out_scales", torch.float32, (layout.T, scale_columns(layout.H)),
+          allow_none=out_q is None)
+    _need(residual, "residual", dtype, rows, allow_none=sum_out is None)
+    _need(sum_out, "sum_out", dtype, rows, allow_none=residual is None)
+    _check(lib.ep_rms_norm(C.byref(layout), _ptr(x), _ptr(residual), _ptr(weight), eps,
+                           _ptr(sum_out), _ptr(out), _ptr(out_q), _ptr(out_scales),
+                           _stream(stream)), "ep_rms_norm")
+
+
+def new_rms_norm_bwd_workspace(layout: Layout, device=None) -> torch.Tensor:
+    """The workspace of ``rms_norm_bwd`` for ``layout`` (uint8 tensor)."""
+    n = int(lib.ep_rms_norm_bwd_workspace(C.byref(layout)))
+    if n == 0:
+        raise ValueError("invalid layout")
+    return torch.empty(n, dtype=torch.uint8, device=device or "cuda")
+
+
+def rms_norm_bwd(layout: Layout, grad: torch.Tensor, x: torch.Tensor, weight: torch.Tensor,
+                 eps: float, grad_x: torch.Tensor, grad_weight: Optional[torch.Tensor] = None,
+                 workspace: Optional[torch.Tensor] = None,
+                 grad_sum: Optional[torch.Tensor] = None, stream=None):
+    """The gradients of ``rms_norm``'s out with respect to what the norm was of
+    (x, or sum_out with a residual) and the weight; grad_sum is a gradient of
+    sum_out that is added to the first. A grad_weight that is None is skipped, and
+    needs no workspace."""
+    rows, dtype = (layout.T, layout.H), layout.payload_dtype
+    _need(grad, "grad", dtype, rows)
+    _need(x, "x", dtype, rows)
+    _need(weight, "weight", dtype, (layout.H,))
+    _need(grad_x, "grad_x", dtype, rows)
+    _need(grad_weight, "grad_weight", dtype, (layout.H,), allow_none=True)
+    _need(workspace, "workspace", torch.uint8, allow_none=grad_weight is None)
+    _need(grad_sum, "grad_sum", dtype, rows, allow_none=True)
+    _check(lib.ep_rms_norm_bwd(C.byref(layout), _ptr(grad), _ptr(grad_sum), _ptr(x),
+                               _ptr(weight), eps, _ptr(grad_x), _ptr(grad_weight),
+                               _ptr(workspace), 0 if workspace is None else workspace.numel(),
+                               _stream(stream)), "ep_rms_norm_bwd")
+
+
+def swiglu_scaled(layout: Layout, handle: torch.Tensor, gate_up: torch.Tensor,
+                  out_q: torch.Tensor, out_scales: torch.Tensor, stream=None):
+    """``swiglu`` with its result in 8 bits: out_q [cap,H] and out_scales
+    [cap, scale_columns(H)]."""
+    _need(handle, "handle", torch.uint8)
+    _need(gate_up, "gate_up", layout.payload_dtype, (layout.cap, 2 * layout.H))
+    _need(out_q, "out_q", E4M3, (layout.cap, layout.H))
+    _need(out_scales, "out_scales", torch.float32, (layout.cap, scale_columns(layout.H)))
+    _check(lib.ep_swiglu_scaled(C.byref(layout), _ptr(handle), handle.numel(), _ptr(gate_up),
+                                _ptr(out_q), _ptr(out_scales), _stream(stream)),
+           "ep_swiglu_scaled")
+
+
+def grouped_linear_scaled(layout: Layout, handle: torch.Tensor, x: torch.Tensor,
+                          x_scales: torch.Tensor, weight: torch.Tensor,
+                          weight_scales: torch.Tensor, out: torch.Tensor, stream=None):
+    """``grouped_linear`` of 8-bit operands: x [cap,H] with x_scales
+    [cap, scale_columns(H)], weight [E,N,H] with weight_scales
+    [E, ceil(N/128), ceil(H/128)]; out [cap,N] of the layout's payload type."""
+    N = _out_features(weight)
+    _need(handle, "handle", torch.uint8)
+    _need(x, "x", E4M3, (layout.cap, layout.H))
+    _need(x_scales, "x_scales", torch.float32, (layout.cap, scale_columns(layout.H)))
+    _need(weight, "weight", E4M3, (layout.E, N, layout.H))
+    _need(weight_scales, "weight_scales", torch.float32,
+          (layout.E, _scale_blocks(N), _scale_blocks(layout.H)))
+    _need(out, "out", layout.payload_dtype, (layout.cap, N))
+    _check(lib.ep_grouped_linear_scaled(C.byref(layout), _ptr(handle), handle.numel(), _ptr(x),
+                                        _ptr(x_scales), _ptr(weight), _ptr(weight_scales),
+                                        _ptr(out), N, _stream(stream)),
+           "ep_grouped_linear_scaled")
+
+
+def new_expert_layer_workspace(layout: Layout, inner: int, device=None) -> torch.Tensor:
+    """The workspace of ``expert_layer`` for ``layout`` and ``inner`` features
+    between the products (uint8 tensor)."""
+    n = int(lib.ep_expert_layer_workspace(C.byref(layout), inner))
+    if n == 0:
+        raise ValueError("invalid layout or inner")
+    return torch.empty(n, dtype=torch.uint8, device=device or "cuda")
+
+
+def expert_layer(layout: Layout, topk_idx: torch.Tensor, topk_weights: torch.Tensor,
+                 tokens: torch.Tensor, gate_up: torch.Tensor, down: torch.Tensor,
+                 result: torch.Tensor, workspace: torch.Tensor,
+                 gate_up_scales: Optional[torch.Tensor] = None,
+                 down_scales: Optional[torch.Tensor] = None, stream=None):
+    """A whole expert layer for a few tokens (T * K up to MAX_LAYER_ROUTES),
+    without a handle: result [T,H] = each token's routes, weighted, through
+    gate_up [E,2I,H], the gated activation and down [E,H,I]. Weights of the
+    payload type, or in 8 bits with both scales."""
+    if down.dim() != 3:
+        raise ValueError(f"down must have shape (E, H, I), got {tuple(down.shape)}")
+    E, H, inner, dtype = layout.E, layout.H, down.shape[2], layout.payload_dtype
+    eight = gate_up_scales is not None or down_scales is not None
+    _need(topk_idx, "topk_idx", torch.int64, (layout.T, layout.K))
+    _need(topk_weights, "topk_weights", torch.float32, (layout.T, layout.K))
+    _need(tokens, "tokens", dtype, (layout.T, H))
+    _need(gate_up, "gate_up", E4M3 if eight else dtype, (E, 2 * inner, H))
+    _need(down, "down", E4M3 if eight else dtype, (E, H, inner))
+    _need(gate_up_scales, "gate_up_scales", torch.float32,
+          (E, _scale_blocks(2 * inner), _scale_blocks(H)), allow_none=not eight)
+    _need(down_scales, "down_scales", torch.float32,
+          (E, _scale_blocks(H), _scale_blocks(inner)), allow_none=not eight)
+    _need(result, "result", dtype, (layout.T, H))
+    _need(workspace, "workspace", torch.uint8)
+    _check(lib.ep_expert_layer(C.byref(layout), _ptr(topk_idx), _ptr(topk_weights),
+                               _ptr(tokens), _ptr(gate_up), _ptr(gate_up_scales), _ptr(down),
+                               _ptr(down_scales), _ptr(result), inner, _ptr(workspace),
+                               workspace.numel(), _stream(stream)), "ep_expert_layer")
 
 
 def read_status(handle: torch.Tensor, stream=None) -> int:

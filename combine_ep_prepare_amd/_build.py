@@ -20,7 +20,8 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 SOURCES = [os.path.join(CSRC, f) for f in ("ep_api.hip", "ep_kernels.hip", "ep_linear.hip",
-                                           "ep_decode.hip", "ep_swiglu.hip")]
+                                           "ep_decode.hip", "ep_swiglu.hip", "ep_scaled.hip",
+                                           "ep_norm.hip", "ep_layer.hip")]
 LIB_NAME = "libcombine_ep_prepare_amd.so"
 LIB = os.path.join(HERE, LIB_NAME)
 CEILINGS_SOURCE = os.path.join(CSRC, "ep_ceilings.hip")

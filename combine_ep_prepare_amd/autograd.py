@@ -34,6 +34,12 @@ work between dispatch and combine: each expert's weights applied to its
 segment, and the gated activation. They read and write live rows only, so
 they give the same results with either policy. Their gradients are not
 differentiable again: a backward with ``create_graph=True`` is refused.
+
+`rms_norm` is the norm in front of a layer. For serving in 8 bits, without a
+backward: `rms_norm_scaled`, `dispatch_scaled`, `grouped_linear_scaled` and
+`swiglu_scaled` take its place and those of the ops above, and `expert_layer`
+runs a whole layer for a few tokens without a routing. They refuse inputs that
+require a gradient.
 """
 from __future__ import annotations
 
@@ -41,13 +47,16 @@ from typing import Optional
 
 import torch
 
-from . import (Layout, combine as _combine, combine_bwd as _combine_bwd,
+from . import (E4M3, Layout, combine as _combine, combine_bwd as _combine_bwd,
                combine_weighted as _combine_weighted,
                combine_weighted_bwd as _combine_weighted_bwd, dispatch as _dispatch,
-               dispatch_bwd as _dispatch_bwd, grouped_linear as _grouped_linear,
-               grouped_linear_bwd as _grouped_linear_bwd,
-               grouped_linear_quant as _grouped_linear_quant, new_handle, prepare,
-               recv_capacity_worst, swiglu as _swiglu, swiglu_bwd as _swiglu_bwd)
+               dispatch_bwd as _dispatch_bwd, expert_layer as _expert_layer,
+               grouped_linear as _grouped_linear, grouped_linear_bwd as _grouped_linear_bwd,
+               grouped_linear_quant as _grouped_linear_quant,
+               grouped_linear_scaled as _grouped_linear_scaled, new_expert_layer_workspace,
+               new_handle, new_rms_norm_bwd_workspace, prepare, recv_capacity_worst,
+               rms_norm as _rms_norm, rms_norm_bwd as _rms_norm_bwd, scale_columns,
+               swiglu as _swiglu, swiglu_bwd as _swiglu_bwd, swiglu_scaled as _swiglu_scaled)
 
 
 class EpRouting:
@@ -219,6 +228,44 @@ class _SwiGLU(torch.autograd.Function):
         return grad_gate_up, None
 
 
+def _norm_layout(x: torch.Tensor) -> Layout:
+    return Layout(x.shape[0], 1, 1, 1, x.shape[1], 0, dtype=x.dtype)
+
+
+class _RmsNorm(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, weight, residual, eps: float):
+        x, weight = x.contiguous(), weight.contiguous()
+        out = torch.empty_like(x)
+        if residual is None:
+            total = x
+            _rms_norm(_norm_layout(x), x, weight, eps, out=out)
+        else:
+            total = torch.empty_like(x)
+            _rms_norm(_norm_layout(x), x, weight, eps, out=out, residual=residual.contiguous(),
+                      sum_out=total)
+        ctx.eps = eps
+        ctx.save_for_backward(total, weight)
+        ctx.set_materialize_grads(False)      # an unused output's gradient stays None
+        return out if residual is None else (out, total)
+
+    @staticmethod
+    def backward(ctx, grad, grad_sum=None):
+        _first_order_only("rms_norm")
+        x, weight = ctx.saved_tensors
+        want_w = ctx.needs_input_grad[1]
+        grad_x, grad_w = grad_sum, None
+        if grad is not None:
+            L = _norm_layout(x)
+            grad_x = torch.empty_like(x)
+            grad_w = torch.empty_like(weight) if want_w else None
+            _rms_norm_bwd(L, grad.contiguous(), x, weight, ctx.eps, grad_x, grad_w,
+                          new_rms_norm_bwd_workspace(L, x.device) if want_w else None,
+                          None if grad_sum is None else grad_sum.contiguous())
+        return (grad_x if ctx.needs_input_grad[0] else None, grad_w,
+                grad_x if ctx.needs_input_grad[2] else None, None)
+
+
 def dispatch(tokens: torch.Tensor, topk_weights: torch.Tensor, routing: EpRouting):
     """(recv_tokens [cap,H], recv_topk_weights [cap]); rows past the live total
     are zeros (unless the routing was made with ``zero_tail=False``)."""
@@ -269,4 +316,104 @@ def grouped_linear_quant(x: torch.Tensor, qweight: torch.Tensor, scales: torch.T
     _grouped_linear_quant(L, routing.handle, x.contiguous(), qweight.contiguous(),
                           scales.contiguous(), None if zeros is None else zeros.contiguous(),
                           out)
+    return out
+
+
+def _serving_only(name: str, *tensors: Optional[torch.Tensor]):
+    if torch.is_grad_enabled() and any(t is not None and t.requires_grad for t in tensors):
+        raise RuntimeError(f"{name} has no backward: call it under torch.no_grad() or on inputs "
+                           "that do not require a gradient")
+
+
+def rms_norm(x: torch.Tensor, weight: torch.Tensor, eps: float,
+             residual: Optional[torch.Tensor] = None):
+    """The norm of the rows of x [T,H] times weight [H]. With a residual: of
+    x + residual, and the pair (norm, sum)."""
+    _rows(x, "x")
+    return _RmsNorm.apply(x, weight, residual, eps)
+
+
+def rms_norm_scaled(x: torch.Tensor, weight: torch.Tensor, eps: float,
+                    residual: Optional[torch.Tensor] = None):
+    """``rms_norm`` in 8 bits: (q, scales), with a residual (q, scales, sum)."""
+    _rows(x, "x")
+    _serving_only("rms_norm_scaled", x, weight, residual)
+    x = x.contiguous()
+    q = torch.empty(x.shape, dtype=E4M3, device=x.device)
+    scales = torch.empty(x.shape[0], scale_columns(x.shape[1]), device=x.device)
+    total = None if residual is None else torch.empty_like(x)
+    _rms_norm(_norm_layout(x), x, weight.contiguous(), eps, out_q=q, out_scales=scales,
+              residual=None if residual is None else residual.contiguous(), sum_out=total)
+    return (q, scales) if residual is None else (q, scales, total)
+
+
+def dispatch_scaled(q: torch.Tensor, scales: torch.Tensor, topk_weights: torch.Tensor,
+                    routing: EpRouting):
+    """``dispatch`` of 8-bit rows [T,H] with their scales [T, scale_columns(H)]:
+    (recv_q, recv_scales, recv_topk_weights), bit copies."""
+    _rows(q, "q")
+    _rows(scales, "scales")
+    _serving_only("dispatch_scaled", topk_weights)
+    if q.dtype != E4M3 or scales.shape[1] != scale_columns(q.shape[1]):
+        raise ValueError(f"{tuple(q.shape)} {q.dtype} and scales {tuple(scales.shape)} are not "
+                         "rows in 8 bits with their scales")
+    rows = q.contiguous().view(torch.bfloat16)
+    L = routing.layout_for(torch.bfloat16, rows.shape[1])
+    LS = routing.layout_for(torch.float32, scales.shape[1])
+    recv = torch.empty(L.cap, L.H, dtype=torch.bfloat16, device=q.device)
+    recv_scales = torch.empty(L.cap, LS.H, device=q.device)
+    recv_w = torch.empty(L.cap, dtype=torch.float32, device=q.device)
+    _dispatch(L, routing.handle, rows, topk_weights.contiguous(), recv, recv_w)
+    _dispatch(LS, routing.handle, scales.contiguous(), None, recv_scales)
+    return recv.view(E4M3), recv_scales, recv_w
+
+
+def grouped_linear_scaled(x: torch.Tensor, x_scales: torch.Tensor, weight: torch.Tensor,
+                          weight_scales: torch.Tensor, routing: EpRouting,
+                          dtype: torch.dtype = torch.bfloat16) -> torch.Tensor:
+    """``grouped_linear`` of 8-bit operands (the binding's layout of their scales)
+    with a result of ``dtype`` (bf16 or fp16): [cap,N]."""
+    _rows(x, "x")
+    _serving_only("grouped_linear_scaled", x_scales, weight_scales)
+    if weight.dim() != 3:
+        raise ValueError(f"weight must have shape (E, N, H), got {tuple(weight.shape)}")
+    L = routing.layout_for(dtype, x.shape[1])
+    out = torch.empty(L.cap, weight.shape[1], dtype=dtype, device=x.device)
+    _grouped_linear_scaled(L, routing.handle, x.contiguous(), x_scales.contiguous(),
+                           weight.contiguous(), weight_scales.contiguous(), out)
+    return out
+
+
+def swiglu_scaled(gate_up: torch.Tensor, routing: EpRouting):
+    """``swiglu`` in 8 bits: (q [cap,I], scales [cap, scale_columns(I)])."""
+    _rows(gate_up, "gate_up")
+    _serving_only("swiglu_scaled", gate_up)
+    L = routing.layout_for(gate_up.dtype, gate_up.shape[1] // 2)
+    q = torch.empty(L.cap, L.H, dtype=E4M3, device=gate_up.device)
+    scales = torch.empty(L.cap, scale_columns(L.H), device=gate_up.device)
+    _swiglu_scaled(L, routing.handle, gate_up.contiguous(), q, scales)
+    return q, scales
+
+
+def expert_layer(tokens: torch.Tensor, topk_idx: torch.Tensor, topk_weights: torch.Tensor,
+                 gate_up: torch.Tensor, down: torch.Tensor,
+                 gate_up_scales: Optional[torch.Tensor] = None,
+                 down_scales: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """A whole expert layer for a few tokens [T,H], routed by topk_idx and
+    topk_weights [T,K] through gate_up [E,2I,H], the gated activation and down
+    [E,H,I]; with scales, 8-bit weights. It has no backward, and needs no routing."""
+    _rows(tokens, "tokens")
+    _rows(topk_idx, "topk_idx")
+    _serving_only("expert_layer", tokens, topk_weights, gate_up, down, gate_up_scales,
+                  down_scales)
+    if down.dim() != 3:
+        raise ValueError(f"down must have shape (E, H, I), got {tuple(down.shape)}")
+    L = Layout(tokens.shape[0], topk_idx.shape[1], down.shape[0], 1, tokens.shape[1], 0,
+               dtype=tokens.dtype)
+    out = torch.empty(tokens.shape, dtype=tokens.dtype, device=tokens.device)
+    _expert_layer(L, topk_idx.contiguous(), topk_weights.contiguous(), tokens.contiguous(),
+                  gate_up.contiguous(), down.contiguous(), out,
+                  new_expert_layer_workspace(L, down.shape[2], tokens.device),
+                  None if gate_up_scales is None else gate_up_scales.contiguous(),
+                  None if down_scales is None else down_scales.contiguous())
     return out

@@ -11,6 +11,7 @@
 
 #include "ep.h"
 #include "ep_internal.h"
+#include "ep_scaled.h"
 
 using namespace epmi;
 
@@ -133,6 +134,43 @@ ep_status_t payload_common(const ep_layout_t* L, const void* handle_mem, size_t 
 // Feature counts of the experts' products: a multiple of 8 up to
 // EP_MAX_FEATURES, so that an offset inside one tile of rows fits 32 bits.
 bool features_ok(int64_t n) { return n >= 8 && n % 8 == 0 && n <= EP_MAX_FEATURES; }
+
+template <typename... P>
+bool all_aligned16(P... p) {
+  return (aligned16(p) && ...);
+}
+
+// Of a call without a handle: the layout's sizes.
+ep_status_t layout_dims(const ep_layout_t* L, Dims* d) {
+  const ep_status_t st = check_layout(L);
+  if (st == EP_OK) *d = dims_of(L, prep_units(L->num_tokens * (int64_t)L->topk));
+  return st;
+}
+
+// Rows of 8-bit values are whole 16-byte vectors too.
+bool bytes_ok(int64_t n) { return features_ok(n) && n % 16 == 0; }
+
+// The parts of the workspace of the layer for a few tokens.
+struct LayerSpace {
+  size_t act, y, bytes;
+};
+LayerSpace layer_space(const Dims& d, int64_t inner) {
+  const size_t routes = (size_t)(d.T * d.K);
+  LayerSpace s;
+  s.act = align256(sizeof(uint32_t) * (size_t)kLayerCounters);
+  s.y = s.act + align256(routes * (size_t)inner * 2);
+  s.bytes = s.y + align256(routes * (size_t)d.H * sizeof(float));
+  return s;
+}
+ep_status_t layer_dims(const ep_layout_t* L, int64_t inner, bool eight, Dims* d) {
+  const ep_status_t st = layout_dims(L, d);
+  if (st != EP_OK) return st;
+  if (d->dtype == EP_DTYPE_FP32) return EP_ERR_SHAPE;
+  if (d->T * d->K > EP_MAX_LAYER_ROUTES) return EP_ERR_SHAPE;
+  if (!features_ok(d->H) || !features_ok(inner)) return EP_ERR_SHAPE;
+  if (eight && !(bytes_ok(d->H) && bytes_ok(inner))) return EP_ERR_SHAPE;
+  return EP_OK;
+}
 
 }  // namespace
 
@@ -459,6 +497,143 @@ ep_status_t ep_swiglu_bwd(const ep_layout_t* layout, const void* handle_mem,
   return EP_OK;
 }
 
+ep_status_t ep_rms_norm(const ep_layout_t* layout, const void* x, const void* residual,
+                        const void* weight, float eps, void* sum, void* out, uint8_t* out_q,
+                        float* out_scales, hipStream_t stream) {
+  Dims d;
+  int num_cus = 0;
+  ep_status_t st = layout_dims(layout, &d);
+  if (st != EP_OK) return st;
+  if (d.H > EP_MAX_NORM_FEATURES || (out_q && !bytes_ok(d.H))) return EP_ERR_SHAPE;
+  if (!(eps >= 0.f)) return EP_ERR_SHAPE;
+  if (!weight) return EP_ERR_NULL;
+  // rows that there are: with none, every pointer to them may be NULL
+  if (d.T > 0) {
+    if (!x || (!out && !out_q) || (out_q == nullptr) != (out_scales == nullptr) ||
+        (residual == nullptr) != (sum == nullptr))
+      return EP_ERR_NULL;
+  }
+  if (!all_aligned16(x, residual, weight, sum, out, out_q, out_scales)) return EP_ERR_ALIGN;
+  if (d.T == 0) return EP_OK;
+  st = current_device(&num_cus);
+  if (st != EP_OK) return st;
+  const NormArgs a{x, residual, weight, sum, out, out_q, out_scales, eps};
+  return launch_rms_norm(d, a, num_cus, stream) == hipSuccess ? EP_OK : EP_ERR_HIP;
+}
+
+size_t ep_rms_norm_bwd_workspace(const ep_layout_t* layout) {
+  Dims d;
+  if (layout_dims(layout, &d) != EP_OK || d.H > EP_MAX_NORM_FEATURES) return 0;
+  return align256(sizeof(float) * (size_t)norm_bwd_partials(d) * (size_t)d.H);
+}
+
+ep_status_t ep_rms_norm_bwd(const ep_layout_t* layout, const void* grad, const void* grad_sum,
+                            const void* x, const void* weight, float eps, void* grad_x,
+                            void* grad_weight, void* workspace, size_t workspace_bytes,
+                            hipStream_t stream) {
+  Dims d;
+  int num_cus = 0;
+  ep_status_t st = layout_dims(layout, &d);
+  if (st != EP_OK) return st;
+  if (d.H > EP_MAX_NORM_FEATURES || !(eps >= 0.f)) return EP_ERR_SHAPE;
+  if (!weight || (d.T > 0 && (!grad || !x || !grad_x))) return EP_ERR_NULL;
+  if (grad_weight && !workspace) return EP_ERR_NULL;
+  if (grad_weight && workspace_bytes < ep_rms_norm_bwd_workspace(layout))
+    return EP_ERR_WORKSPACE;
+  if (!all_aligned16(grad, grad_sum, x, weight, grad_x, grad_weight, workspace))
+    return EP_ERR_ALIGN;
+  if (d.T == 0 && !grad_weight) return EP_OK;
+  st = current_device(&num_cus);
+  if (st != EP_OK) return st;
+  const NormBwdArgs a{grad,   grad_sum,    x,
+                      weight, grad_x,      grad_weight,
+                      static_cast<float*>(workspace), eps};
+  return launch_rms_norm_bwd(d, a, num_cus, stream) == hipSuccess ? EP_OK : EP_ERR_HIP;
+}
+
+ep_status_t ep_swiglu_scaled(const ep_layout_t* layout, const void* handle_mem,
+                             size_t handle_bytes, const void* gate_up, uint8_t* out_q,
+                             float* out_scales, hipStream_t stream) {
+  Dims d;
+  HandleView hv;
+  int num_cus = 0;
+  ep_status_t st = payload_common(layout, handle_mem, handle_bytes, &d, &hv);
+  if (st != EP_OK) return st;
+  if (!bytes_ok(d.H)) return EP_ERR_SHAPE;
+  if (d.cap > 0 && (!gate_up || !out_q || !out_scales)) return EP_ERR_NULL;
+  if (!all_aligned16(gate_up, out_q, out_scales)) return EP_ERR_ALIGN;
+  st = current_device(&num_cus);
+  if (st != EP_OK) return st;
+  return launch_swiglu_scaled(d, hv, gate_up, out_q, out_scales, num_cus, stream) == hipSuccess
+             ? EP_OK
+             : EP_ERR_HIP;
+}
+
+ep_status_t ep_grouped_linear_scaled(const ep_layout_t* layout, const void* handle_mem,
+                                     size_t handle_bytes, const uint8_t* x,
+                                     const float* x_scales, const uint8_t* weight,
+                                     const float* weight_scales, void* out,
+                                     int64_t out_features, hipStream_t stream) {
+  Dims d;
+  HandleView hv;
+  int num_cus = 0;
+  ep_status_t st = payload_common(layout, handle_mem, handle_bytes, &d, &hv);
+  if (st != EP_OK) return st;
+  if (!bytes_ok(d.H) || !features_ok(out_features)) return EP_ERR_SHAPE;
+  if (d.dtype == EP_DTYPE_FP32) return EP_ERR_SHAPE;
+  if (!weight || !weight_scales || (d.cap > 0 && (!x || !x_scales || !out))) return EP_ERR_NULL;
+  if (!all_aligned16(x, x_scales, weight, weight_scales, out)) return EP_ERR_ALIGN;
+  st = current_device(&num_cus);
+  if (st != EP_OK) return st;
+  return launch_grouped_scaled(d, hv, x, x_scales, weight, weight_scales, out, out_features,
+                               num_cus, stream) == hipSuccess
+             ? EP_OK
+             : EP_ERR_HIP;
+}
+
+size_t ep_expert_layer_workspace(const ep_layout_t* layout, int64_t inner) {
+  Dims d;
+  if (layer_dims(layout, inner, false, &d) != EP_OK) return 0;
+  return layer_space(d, inner).bytes;
+}
+
+ep_status_t ep_expert_layer(const ep_layout_t* layout, const int64_t* topk_idx,
+                            const float* topk_weights, const void* tokens, const void* gate_up,
+                            const float* gate_up_scales, const void* down,
+                            const float* down_scales, void* result, int64_t inner,
+                            void* workspace, size_t workspace_bytes, hipStream_t stream) {
+  Dims d;
+  int num_cus = 0;
+  if ((gate_up_scales == nullptr) != (down_scales == nullptr)) return EP_ERR_NULL;
+  ep_status_t st = layer_dims(layout, inner, gate_up_scales != nullptr, &d);
+  if (st != EP_OK) return st;
+  if (!gate_up || !down) return EP_ERR_NULL;
+  if (d.T > 0 && (!topk_idx || !topk_weights || !tokens || !result || !workspace))
+    return EP_ERR_NULL;
+  const LayerSpace s = layer_space(d, inner);
+  if (d.T > 0 && workspace_bytes < s.bytes) return EP_ERR_WORKSPACE;
+  if (!all_aligned16(topk_idx, topk_weights, tokens, gate_up, gate_up_scales, down, down_scales,
+                   result, workspace))
+    return EP_ERR_ALIGN;
+  if (d.T == 0) return EP_OK;
+  st = current_device(&num_cus);
+  if (st != EP_OK) return st;
+  char* ws = static_cast<char*>(workspace);
+  const LayerArgs a{topk_idx,
+                    topk_weights,
+                    tokens,
+                    gate_up,
+                    gate_up_scales,
+                    down,
+                    down_scales,
+                    result,
+                    reinterpret_cast<uint32_t*>(ws),
+                    ws + s.act,
+                    reinterpret_cast<float*>(ws + s.y),
+                    inner};
+  return launch_expert_layer(d, a, num_cus, stream) == hipSuccess ? EP_OK : EP_ERR_HIP;
+}
+
 ep_status_t ep_read_status(const void* handle_mem, uint32_t* host_out, hipStream_t stream) {
   if (!handle_mem || !host_out) return EP_ERR_NULL;
   if (!aligned16(handle_mem)) return EP_ERR_ALIGN;
@@ -485,6 +660,7 @@ const char* ep_status_str(ep_status_t status) {
     case EP_ERR_HIP: return "a HIP call or kernel launch failed";
     case EP_ERR_SCRATCH:
       return "the layout needs more prepare scratch than ep_prepare_static's static buffer holds";
+    case EP_ERR_WORKSPACE: return "workspace_bytes is below what the call's query returns";
   }
   return "unknown ep_status_t";
 }

@@ -1,0 +1,242 @@
+// ep_lines.h -- weights streamed once for up to 16 rows of x, a wavefront at a
+// time: the inner part of the products for few rows (ep_scaled.hip, ep_layer.hip).
+//
+// A handful of rows uses every weight once, so the weights' bytes bound it. A
+// step of a wavefront is 128 bytes of each of a tile's columns (rows of the weight
+// matrix). A load takes 8 columns x 128 bytes: whole lines, each asked for once,
+// so that they can pass the caches by. A lane of a matrix instruction wants 16
+// bytes of column lane % 16 instead, so the lines go from registers through a part
+// of LDS that belongs to the wavefront alone, with no barrier: chunk c of column n
+// at slot c ^ (n & 7). While a step is multiplied out of LDS, the next one's loads
+// are in flight.
+#pragma once
+
+#include "ep_experts.h"
+#include "ep_scaled.h"
+
+namespace epmi {
+
+namespace {
+
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+typedef int i32x8 __attribute__((ext_vector_type(8)));
+typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
+typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
+
+template <int DT>
+__device__ __forceinline__ f32x4 mma16(row16_t n, row16_t m, f32x4 acc) {
+  if constexpr (DT == EP_DTYPE_BF16) {
+    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(
+        __builtin_bit_cast(bf16x8, n), __builtin_bit_cast(bf16x8, m), acc, 0, 0, 0);
+  } else {
+    return __builtin_amdgcn_mfma_f32_16x16x32_f16(
+        __builtin_bit_cast(f16x8, n), __builtin_bit_cast(f16x8, m), acc, 0, 0, 0);
+  }
+}
+
+// A whole block of 128 e4m3 values of k at once: 32 a lane, in two halves.
+__device__ __forceinline__ f32x4 mma8(row16_t n0, row16_t n1, row16_t m0, row16_t m1) {
+  struct Both { row16_t a, b; };
+  const f32x4 zero = {0.f, 0.f, 0.f, 0.f};
+  return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
+      __builtin_bit_cast(i32x8, Both{n0, n1}), __builtin_bit_cast(i32x8, Both{m0, m1}), zero, 0,
+      0, 0, 0, 0, 0);
+}
+
+// Eight e4m3 values to the payload type, exactly (both types hold them all).
+template <int DT>
+__device__ __forceinline__ row16_t widen8(uint32_t lo, uint32_t hi) {
+  if constexpr (DT == EP_DTYPE_BF16) {
+    return row16_t{
+        __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, 1.f, false)),
+        __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, 1.f, true)),
+        __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, 1.f, false)),
+        __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, 1.f, true))};
+  } else {
+    return row16_t{
+        __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(lo, 1.f, false)),
+        __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(lo, 1.f, true)),
+        __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(hi, 1.f, false)),
+        __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(hi, 1.f, true))};
+  }
+}
+
+// Four sums rounded to a 16-bit payload type.
+template <int DT>
+__device__ __forceinline__ u32x2 round_four(f32x4 v) {
+  if constexpr (DT == EP_DTYPE_BF16) {
+    return u32x2{rne_bf16(v[0]) | (rne_bf16(v[1]) << 16),
+                 rne_bf16(v[2]) | (rne_bf16(v[3]) << 16)};
+  } else {
+    return u32x2{rne_f16(v[0]) | (rne_f16(v[1]) << 16), rne_f16(v[2]) | (rne_f16(v[3]) << 16)};
+  }
+}
+
+// Operands of a product for few rows.
+enum Form {
+  kPayload,   // weights and x of the payload type
+  kScaled,    // weights and x in 8 bits, each with scales
+  kWeights8   // weights in 8 bits with scales, x of the payload type: a block's
+              // sum is that of the e4m3 values themselves, and scaled in fp32
+};
+
+// A tile has COLS columns in two halves, which may lie apart (gate and up rows).
+template <int F, int DT, int COLS>
+struct Lines {
+  static constexpr int kSize = F == kPayload ? 2 : 1;       // bytes of a weight
+  static constexpr int kStep = 128 / kSize;                 // values of k
+  static constexpr int kLoads = COLS / 8;
+  static constexpr int kNF = COLS / 16;                     // blocks of 16 columns
+  static constexpr int kX = F == kWeights8 ? 4 : 2;         // 16-byte parts of x
+  static constexpr int kXSize = F == kScaled ? 1 : 2;
+  static constexpr int kScales = F == kPayload ? 0 : F == kScaled ? 1 : kNF;
+  static constexpr int kLds = COLS * 128;
+  static constexpr int kSumRow = COLS + 4;                  // floats of a row of sums
+  static_assert(16 * kSumRow * 4 <= kLds, "the sums fit the weights' place");
+
+  struct Source {
+    const char* w[2];            // first column of either half, the same in all lanes
+    int32_t cols[2];             // columns of either half that there are, multiples of 8
+    const char* x;               // the lane's row of x
+    const float* x_scales;       // its scales (kScaled)
+    const float* w_scales[kScales > 0 ? kScales : 1];   // of the lane's columns
+  };
+
+  row16_t w[kLoads];
+  row16_t x[kX];
+  float scale[kScales > 0 ? kScales : 1];
+  float x_scale;
+
+  // The k, in the step, of part p of this lane's x: the same as that of the
+  // weights that multiply() reads beside it.
+  __device__ static __forceinline__ int32_t input(int p) {
+    const int q = lane_id() >> 4;
+    if constexpr (F == kPayload) return 32 * p + 8 * q;
+    if constexpr (F == kScaled) return 64 * p + 16 * q;
+    return 64 * (p / 2) + 16 * q + 8 * (p % 2);
+  }
+
+  // Loads of the step that starts at k0. In one that passes the end of the rows
+  // (PART) a lane whose bytes are not there reads the rows' start and takes it
+  // out again, of the weights and of x, whatever that holds.
+  template <bool PART>
+  __device__ __forceinline__ void load(const Source& s, int32_t k0, int32_t K) {
+    const int lane = lane_id();
+    const uint32_t w_row = (uint32_t)K * kSize;
+    const int chunk = (lane & 7) ^ (lane >> 3);
+    const bool in = !PART || k0 + chunk * (kStep / 8) < K;
+    const uint32_t at = (uint32_t)(lane >> 3) * w_row + (in ? (uint32_t)(k0 * kSize + chunk * 16) : 0u);
+    static_for<kLoads>([&](auto j) {
+      constexpr int half = j / (kLoads / 2), jj = j % (kLoads / 2);
+      const char* column = s.w[half] + (jj * 8 < s.cols[half] ? jj * 8 * (int64_t)w_row : 0);
+      w[j] = __builtin_nontemporal_load(reinterpret_cast<const row16_t*>(column + at));
+      if constexpr (PART) w[j] = in ? w[j] : row16_t{0, 0, 0, 0};
+    });
+    static_for<kX>([&](auto p) {
+      const int32_t k = k0 + input(p);
+      const bool have = !PART || k < K;
+      x[p] = *reinterpret_cast<const row16_t*>(s.x + (have ? (int64_t)k * kXSize : 0));
+      if constexpr (PART) x[p] = have ? x[p] : row16_t{0, 0, 0, 0};
+    });
+    if constexpr (F != kPayload) {
+      const int32_t block = k0 / kScaleBlock;
+      static_for<kScales>([&](auto i) { scale[i] = s.w_scales[i][block]; });
+      if constexpr (F == kScaled) x_scale = s.x_scales[block];
+    }
+  }
+
+  // The loaded weights into the wavefront's LDS. Its lanes write and read it in
+  // program order; the fences keep the compiler to it.
+  __device__ __forceinline__ void put(char* lds) const {
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    static_for<kLoads>([&](auto j) {
+      *reinterpret_cast<row16_t*>(lds + j * 1024 + lane_id() * 16) = w[j];
+    });
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+  }
+
+  // Multiplies the loaded step; with MORE, the whole step from k1 on is asked for
+  // as soon as the registers are free.
+  template <bool MORE>
+  __device__ __forceinline__ void step(char* lds, const Source& s, int32_t k1, int32_t K,
+                                       f32x4 (&acc)[kNF]) {
+    put(lds);
+    row16_t xs[kX];
+    static_for<kX>([&](auto p) { xs[p] = x[p]; });
+    float sc[kScales > 0 ? kScales : 1];
+    static_for<kScales>([&](auto i) { sc[i] = F == kScaled ? scale[i] * x_scale : scale[i]; });
+    if constexpr (MORE) load<false>(s, k1, K);
+    const int lane = lane_id(), q = lane >> 4, i16 = lane & 15;
+    const char* mine = lds + i16 * 128;
+    const int slot0 = (q ^ (i16 & 7)) << 4, slot1 = ((4 + q) ^ (i16 & 7)) << 4;
+    static_for<kNF>([&](auto j) {
+      const row16_t a = *reinterpret_cast<const row16_t*>(mine + j * 2048 + slot0);
+      const row16_t b = *reinterpret_cast<const row16_t*>(mine + j * 2048 + slot1);
+      if constexpr (F == kPayload) {
+        acc[j] = mma16<DT>(a, xs[0], acc[j]);
+        acc[j] = mma16<DT>(b, xs[1], acc[j]);
+      } else {
+        f32x4 part;
+        if constexpr (F == kScaled) {
+          part = mma8(a, b, xs[0], xs[1]);
+        } else {
+          part = f32x4{0.f, 0.f, 0.f, 0.f};
+          part = mma16<DT>(widen8<DT>(a[0], a[1]), xs[0], part);
+          part = mma16<DT>(widen8<DT>(a[2], a[3]), xs[1], part);
+          part = mma16<DT>(widen8<DT>(b[0], b[1]), xs[2], part);
+          part = mma16<DT>(widen8<DT>(b[2], b[3]), xs[3], part);
+        }
+        static_for<4>([&](auto c) {
+          acc[j][c.value] =
+              __builtin_fmaf(sc[F == kScaled ? 0 : j.value], part[c.value], acc[j][c.value]);
+        });
+      }
+    });
+  }
+
+  // All steps of a tile that are this wavefront's: every `waves`-th of them,
+  // the first of which, if whole, has been asked for.
+  __device__ __forceinline__ void steps(char* lds, const Source& s, int wave, int waves, int32_t K,
+                                        f32x4 (&acc)[kNF]) {
+    const int32_t full = K / kStep, stride = waves * kStep;
+    if (wave < full) {
+      int32_t k = wave * kStep;
+      for (; k + stride < full * kStep; k += stride) step<true>(lds, s, k + stride, K, acc);
+      step<false>(lds, s, 0, K, acc);
+    }
+    if (full * kStep < K && wave == full % waves) {
+      load<true>(s, full * kStep, K);
+      step<false>(lds, s, 0, K, acc);
+    }
+  }
+  __device__ __forceinline__ void first(const Source& s, int wave, int32_t K) {
+    if (wave < K / kStep) load<false>(s, wave * kStep, K);
+  }
+
+  // The wavefront's sums into its LDS: [row][column] of kSumRow floats.
+  __device__ static __forceinline__ void put_sums(char* lds, const f32x4 (&acc)[kNF]) {
+    const int lane = lane_id();
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    static_for<kNF>([&](auto j) {
+      *reinterpret_cast<f32x4*>(lds + ((lane & 15) * kSumRow + j * 16 + (lane >> 4) * 4) * 4) =
+          acc[j];
+    });
+  }
+  // Four columns from n on of row m, added up over the block's wavefronts.
+  template <int WAVES>
+  __device__ static __forceinline__ f32x4 sum_of(const char* mem, int m, int n) {
+    const char* p = mem + (m * kSumRow + n) * 4;
+    f32x4 sum = *reinterpret_cast<const f32x4*>(p);
+    static_for<WAVES - 1>([&](auto v) {
+      sum += *reinterpret_cast<const f32x4*>(p + (v + 1) * kLds);
+    });
+    return sum;
+  }
+};
+
+}  // namespace
+
+}  // namespace epmi

@@ -13,6 +13,8 @@
 // both good to fp32's own precision.
 
 #include "ep_experts.h"
+#include "ep_gate.h"
+#include "ep_quantise.h"
 
 namespace epmi {
 
@@ -23,73 +25,6 @@ constexpr int kBlocksPerCU = 64;
 // Vectors of a block step, at least: a block takes as many whole rows at a
 // time as hold them, so that narrow rows fill its lanes too.
 constexpr int kStepVectors = 8 * kThreads;
-
-// What the results take from a gate g. With e = exp(-|g|) and r = 1 / (1 + e),
-//   s = 1 / (1 + exp(-g)) = p^2 r and 1 - s = q, where
-//   p = 1, q = e r for g >= 0 and p = sqrt(e), q = r for g < 0:
-// no exponential overflows, 1 - s does not cancel, and s enters a product as
-// one p a factor, so that a sigmoid below fp32's range still counts: a gate of
-// -88 gives silu(g) = -5e-37. p is a normal number down to g = -174, past which
-// it is 0.
-struct Gate {
-  float p, q, r;
-};
-
-// The exponent |g| log2(e) / 2 of p is rounded, which takes p off by up to
-// |g| / 2 units of 2^-24: nothing to a 16-bit result (a gate of 174 makes 2^-16
-// of it in s). EXACT, for fp32, carries what the rounding and the constant
-// leave out into p and refines the reciprocal by a step: s is then within 20
-// units of 2^-24 of its value at any g, in the time that the rows' bytes take
-// anyway (8192 rows by top-2, 4096 values out: 146 us with it and without).
-template <bool EXACT>
-__device__ __forceinline__ Gate gate_of(float g) {
-  constexpr double kLog2e = 1.44269504088896340736;
-  constexpr float kHi = (float)kLog2e, kLo = (float)(kLog2e - (double)kHi);
-  constexpr float kHalfLn2 = 0.34657359027997265f;
-  Gate o;
-  float root;   // sqrt(e)
-  if constexpr (EXACT) {
-    // past 400 p is 0, and an infinite g would make the rest a NaN
-    const float x = __builtin_fminf(__builtin_fabsf(g), 400.f);
-    const float a = x * kHi;
-    const float rest = __builtin_fmaf(x, kLo, __builtin_fmaf(x, kHi, -a));
-    root = __builtin_amdgcn_exp2f(a * -0.5f);
-    root = __builtin_fmaf(root, rest * -kHalfLn2, root);
-  } else {
-    root = __builtin_amdgcn_exp2f(__builtin_fabsf(g) * (-0.5f * kHi));
-  }
-  const float e = root * root, d = 1.f + e;
-  o.r = __builtin_amdgcn_rcpf(d);
-  if constexpr (EXACT) o.r = __builtin_fmaf(__builtin_fmaf(-d, o.r, 1.f), o.r, o.r);
-  o.p = g < 0.f ? root : 1.f;
-  o.q = g < 0.f ? o.r : e * o.r;
-  return o;
-}
-
-// Rounds like Payload::pack; where no lane has a NaN, by the hardware's packed
-// conversions.
-template <int DT, int N>
-__device__ __forceinline__ row16_t pack(const float (&o)[N]) {
-  if constexpr (DT != EP_DTYPE_FP32) {
-    bool nan = false;
-    static_for<N / 2>([&](auto j) { nan |= __builtin_isunordered(o[2 * j], o[2 * j + 1]); });
-    if (wave_ballot(nan) == 0) {
-      typedef std::conditional_t<DT == EP_DTYPE_BF16, __bf16, _Float16> half;
-      typedef half half2 __attribute__((ext_vector_type(2)));
-      typedef float float2v __attribute__((ext_vector_type(2)));
-      row16_t v;
-      static_for<4>([&](auto j) {
-        float2v f = {o[2 * j], o[2 * j + 1]};
-        // the fp32 results stand as they are: no fusing of the last product
-        // with the conversion, which would skip its rounding
-        asm("" : "+v"(f));
-        v[j.value] = __builtin_bit_cast(uint32_t, __builtin_convertvector(f, half2));
-      });
-      return v;
-    }
-  }
-  return Payload<DT>::pack(o);
-}
 
 // A thread takes 16 bytes of each half of a row. Rows are dealt in address
 // order; row_src tells which hold a route, the others are zeroed under the
@@ -163,7 +98,98 @@ __global__ void __launch_bounds__(kThreads)
   }
 }
 
+// The activation with its result in 8 bits. The values of a scale lie side by
+// side in a row: 16 (fp32: 32) neighbouring lanes hold them, 16 bytes of each
+// half a lane, and the scale's maximum takes four (five) exchanges. Rows are
+// dealt by such blocks in address order.
+template <int DT>
+__global__ void __launch_bounds__(kThreads)
+    swiglu_scaled_kernel(Dims d, HandleView hv, const row16_t* __restrict__ gate_up,
+                         uint8_t* __restrict__ out_q, float* __restrict__ out_scales,
+                         int32_t step_rows) {
+  const HandleHeader hh = *hv.header;
+  if (!handle_matches(hh, d)) {
+    if (blockIdx.x == 0 && threadIdx.x == 0) atomicOr(&hv.header->status, EP_STATUS_LAYOUT);
+    return;
+  }
+  using P = Payload<DT>;
+  constexpr int N = P::N;
+  constexpr int kLanes = kScaleBlock / N, kGroups = kThreads / kLanes;
+  const int64_t live = hh.total < d.cap ? hh.total : d.cap;
+  const int64_t rows = d.zero_tail ? d.cap : live;
+  const int32_t V = (int32_t)d.V, S = (int32_t)EP_SCALE_COLUMNS(d.H);
+  const int32_t group = threadIdx.x / kLanes, lane = threadIdx.x % kLanes;
+  // S places a row: those past its values hold zeros alone
+  const int32_t row_first = group / S, b_first = group % S;
+  const int32_t row_by = kGroups / S, b_by = kGroups % S;
+  for (int64_t r0 = (int64_t)blockIdx.x * step_rows; r0 < rows;
+       r0 += (int64_t)gridDim.x * step_rows) {
+    const int64_t r1 = r0 + step_rows < rows ? r0 + step_rows : rows;
+    int64_t r = r0 + row_first;
+    int32_t b = b_first;
+    int32_t source = r < r1 && r < live ? hv.row_src[r] : -1;
+    while (r < r1) {
+      int64_t next_r = r + row_by;
+      int32_t next_b = b + b_by;
+      if (next_b >= S) {
+        next_b -= S;
+        ++next_r;
+      }
+      const int32_t next_source = next_r < r1 && next_r < live ? hv.row_src[next_r] : -1;
+      const int32_t v = b * kLanes + lane;
+      const bool in = v < V;
+      uint32_t q[N / 4] = {};
+      float scale = 0.f;
+      if (source >= 0 && b * kLanes < V) {
+        row16_t gv = {0, 0, 0, 0}, uv = {0, 0, 0, 0};
+        if (in) {
+          gv = __builtin_nontemporal_load(gate_up + r * 2 * V + v);
+          uv = __builtin_nontemporal_load(gate_up + r * 2 * V + V + v);
+        }
+        float o[N], amax = 0.f;
+        static_for<N>([&](auto j) {
+          const float g = P::template get<j>(gv);
+          const Gate k = gate_of<DT == EP_DTYPE_FP32>(g);
+          o[j] = g * k.p * k.r * (P::template get<j>(uv) * k.p);
+          amax = __builtin_fmaxf(amax, finite_magnitude(o[j]));
+        });
+        const BlockScale s = block_scale(group_max<kLanes>(amax));
+        scale = s.scale;
+        static_for<N / 4>([&](auto j) {
+          q[j] = to_e4m3(o[4 * j] * s.by, o[4 * j + 1] * s.by, o[4 * j + 2] * s.by,
+                         o[4 * j + 3] * s.by);
+        });
+      }
+      if (source >= 0 || r >= live || d.fill_pads) {
+        if (in) {
+          uint32_t* to = reinterpret_cast<uint32_t*>(out_q + r * d.H) + (int64_t)v * (N / 4);
+          static_for<N / 4>([&](auto j) { to[j] = q[j]; });
+        }
+        if (lane == 0) out_scales[r * S + b] = scale;
+      }
+      r = next_r;
+      b = next_b;
+      source = next_source;
+    }
+  }
+}
+
 }  // namespace
+
+hipError_t launch_swiglu_scaled(const Dims& d, const HandleView& hv, const void* gate_up,
+                                uint8_t* out_q, float* out_scales, int num_cus,
+                                hipStream_t stream) {
+  const int32_t step_rows = (int32_t)((kStepVectors + d.V - 1) / d.V);
+  int64_t blocks = (d.cap + step_rows - 1) / step_rows;
+  const int64_t most = (int64_t)num_cus * kBlocksPerCU;
+  if (blocks > most) blocks = most;
+  if (blocks < 1) blocks = 1;
+  return with_payload(d.dtype, [&](auto dt) {
+    swiglu_scaled_kernel<decltype(dt)::value><<<dim3((uint32_t)blocks), dim3(kThreads), 0, stream>>>(
+        d, hv, static_cast<const row16_t*>(gate_up), out_q, out_scales, step_rows);
+    return hipGetLastError();
+  });
+}
 
 hipError_t launch_swiglu(const Dims& d, const HandleView& hv, bool backward, const void* grad,
                          const void* gate_up, void* out, int num_cus, hipStream_t stream) {

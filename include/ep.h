@@ -3,7 +3,9 @@
  * (gfx950): prepare, dispatch, combine and their two backward ops, plus a
  * fused weighted combine and its backward, and the experts' own work between
  * dispatch and combine: products grouped by expert, with their gradients and
- * with 4-bit weights, and the gated activation with its gradient.
+ * with 4-bit weights, and the gated activation with its gradient; the same in 8
+ * bits with scales, from the norm in front of the layer on; and a whole layer
+ * for a few tokens.
  *
  * The five per-step calls follow the per-step part of the common C API in
  * "Expert Parallelism: common C API + NCCL EP backend" (section "Per-step
@@ -75,8 +77,11 @@ typedef enum ep_status {
   EP_ERR_CAPACITY = 5,    /* recv_capacity < 0 or >= 2^31 */
   EP_ERR_DEVICE = 6,      /* the current device is not gfx950 */
   EP_ERR_HIP = 7,         /* a HIP runtime call or kernel launch failed */
-  EP_ERR_SCRATCH = 8      /* ep_prepare_static: the layout's prepare scratch
+  EP_ERR_SCRATCH = 8,     /* ep_prepare_static: the layout's prepare scratch
                              exceeds EP_PREPARE_STATIC_SCRATCH_BYTES */
+  EP_ERR_WORKSPACE = 9    /* workspace_bytes is below what the call's query
+                             (ep_rms_norm_bwd_workspace,
+                             ep_expert_layer_workspace) returns */
 } ep_status_t;
 
 /* Sticky device-side bits of a handle's status word. */
@@ -478,6 +483,143 @@ ep_status_t ep_swiglu(const ep_layout_t* layout, const void* handle_mem, size_t 
 ep_status_t ep_swiglu_bwd(const ep_layout_t* layout, const void* handle_mem,
                           size_t handle_bytes, const void* grad, const void* gate_up,
                           void* grad_gate_up, hipStream_t stream);
+
+/*
+ * The layer in 8 bits: rows and weights of e4m3 values (OCP 8-bit floating
+ * point: four bits of exponent, three of mantissa, largest value 448, NaN 0x7F
+ * and 0xFF, no infinity) with fp32 scales; a value stands for q * scale. A row
+ * has one scale for every EP_SCALE_BLOCK of its values, the last block perhaps a
+ * part, and room for EP_SCALE_COLUMNS of them: rows of scales are whole 16-byte
+ * vectors this way, and ep_dispatch moves them as fp32 rows of that many values
+ * (and 8-bit rows of H values as bf16 rows of H / 2), bit for bit. Weights
+ * [E,N,H] have one scale for every 128 x 128: fp32 [E, ceil(N/128),
+ * ceil(H/128)].
+ *
+ * Rounding to 8 bits (ep_rms_norm, ep_swiglu_scaled): with y a row's fp32
+ * results and amax the largest magnitude among a block's finite ones,
+ *   scale = max(amax, 448 * 2^-100) / 448,   q = e4m3(y / scale)
+ * to nearest, ties to even (y / scale is taken as y times the fp32 reciprocal of
+ * scale, so that a y within 2^-22 of the middle of two values may go either way).
+ * An infinite or NaN y becomes NaN in its own place. Scale columns past a row's
+ * blocks are +0.
+ */
+#define EP_SCALE_BLOCK 128
+#define EP_SCALE_COLUMNS(H) (((H) + 1023) / 1024 * 8)
+
+/*
+ * Root-mean-square norm of the layout's T token rows, as it stands in front of
+ * dispatch. With a residual,
+ *   sum[t,:] = payload(x[t,:] + residual[t,:]),   s = sum[t,:]
+ * and s = x[t,:] without one; then
+ *   y = s / sqrt(mean(s^2) + eps) * weight
+ * in fp32, given as out (rounded once), as out_q with out_scales, or as both.
+ * The norm is that of the rounded sum, which the gradient is taken at. hidden up
+ * to EP_MAX_NORM_FEATURES; with out_q a multiple of 16; eps 0 or more. Uses the layout's
+ * num_tokens, hidden and dtype.
+ *   x           payload [T,H]
+ *   residual    payload [T,H] or NULL
+ *   weight      payload [H]
+ *   sum         payload [T,H]; NULL iff residual is
+ *   out         payload [T,H] or NULL
+ *   out_q       e4m3 [T,H] or NULL; out and out_q are not both NULL
+ *   out_scales  fp32 [T, EP_SCALE_COLUMNS(H)]; NULL iff out_q is
+ */
+#define EP_MAX_NORM_FEATURES 16384
+
+ep_status_t ep_rms_norm(const ep_layout_t* layout, const void* x, const void* residual,
+                        const void* weight, float eps, void* sum, void* out, uint8_t* out_q,
+                        float* out_scales, hipStream_t stream);
+
+/* Bytes of device memory that ep_rms_norm_bwd needs for its weight gradient, at
+ * most 1024 * H * 4; 0 for an invalid layout. Host only. */
+size_t ep_rms_norm_bwd_workspace(const ep_layout_t* layout);
+
+/*
+ * Backward of the norm, with r = 1 / sqrt(mean(s^2) + eps) and n = s r:
+ *   grad_x[t,:]     = r (g - n mean(g n)) + grad_sum[t,:],  g = grad[t,:] * weight
+ *   grad_weight[:]  = sum over t of grad[t,:] * n
+ * grad_x is the gradient of x and of the residual alike. grad_weight is summed in
+ * fp32 in an order that the sizes fix, and written whole (+0 for T = 0).
+ *   grad         payload [T,H]   of out
+ *   grad_sum     payload [T,H]   of sum, or NULL
+ *   x            payload [T,H]   what the norm was of: sum with a residual, else x
+ *   weight       payload [H]
+ *   grad_x       payload [T,H]
+ *   grad_weight  payload [H] or NULL (skipped; workspace may be NULL then)
+ *   workspace    workspace_bytes of device memory, rewritten here: calls that
+ *                share one must be ordered on the GPU
+ */
+ep_status_t ep_rms_norm_bwd(const ep_layout_t* layout, const void* grad, const void* grad_sum,
+                            const void* x, const void* weight, float eps, void* grad_x,
+                            void* grad_weight, void* workspace, size_t workspace_bytes,
+                            hipStream_t stream);
+
+/*
+ * ep_swiglu with its result in 8 bits. I = layout->hidden, a multiple of 16. Pad
+ * and tail rows of out_q and out_scales follow the layout's flags as every
+ * expert-major output does.
+ *   gate_up     payload [recv_capacity,2I]
+ *   out_q       e4m3 [recv_capacity,I]
+ *   out_scales  fp32 [recv_capacity, EP_SCALE_COLUMNS(I)]
+ */
+ep_status_t ep_swiglu_scaled(const ep_layout_t* layout, const void* handle_mem,
+                             size_t handle_bytes, const void* gate_up, uint8_t* out_q,
+                             float* out_scales, hipStream_t stream);
+
+/*
+ * Grouped linear of 8-bit operands: ep_grouped_linear of the values that x and
+ * weight stand for, the scales applied in fp32 to the sums over a block, out
+ * rounded once to the payload type (bf16 or fp16; fp32 is EP_ERR_SHAPE). A block's
+ * sum is that of the 8-bit matrix instruction, which cuts products off 13 bits
+ * below the largest of the eight neighbours that it adds first; from there on sums
+ * are fp32. For serving, with no backward. H = layout->hidden is a multiple of 16, N =
+ * out_features of 8.
+ *   x              e4m3 [recv_capacity,H]
+ *   x_scales       fp32 [recv_capacity, EP_SCALE_COLUMNS(H)]
+ *   weight         e4m3 [E,N,H]
+ *   weight_scales  fp32 [E, ceil(N/128), ceil(H/128)]
+ *   out            payload [recv_capacity,N]
+ */
+ep_status_t ep_grouped_linear_scaled(const ep_layout_t* layout, const void* handle_mem,
+                                     size_t handle_bytes, const uint8_t* x,
+                                     const float* x_scales, const uint8_t* weight,
+                                     const float* weight_scales, void* out,
+                                     int64_t out_features, hipStream_t stream);
+
+/*
+ * A whole expert layer for a few tokens, without a prepared handle: for every
+ * token, over its valid routes k ascending, with e = topk_idx[t,k],
+ *   a         = payload(silu(gate_up[e,:I,:] x) * (gate_up[e,I:,:] x)),  x = tokens[t,:]
+ *   result[t] = payload(sum over k of topk_weights[t,k] * (down[e] a))
+ * the products and the weighted sum in fp32 (the first term a product, each later
+ * one a fused multiply-add). A route whose id is outside [0,E), masked or not,
+ * counts nothing; a token with no valid route gets +0; an expert may come more
+ * than once. T*K is at most EP_MAX_LAYER_ROUTES; uses the layout's num_tokens,
+ * topk, num_experts, hidden and dtype (bf16 or fp16; fp32 is EP_ERR_SHAPE). For
+ * serving, with no backward. The weights are of the payload type, or, with both
+ * scales given, e4m3 with 128 x 128 scales (hidden and inner multiples of 16
+ * then); their values enter the products exactly and the scales the fp32 sums.
+ *   topk_idx        int64 [T,K]
+ *   topk_weights    fp32 [T,K]
+ *   tokens          payload [T,H]
+ *   gate_up         payload or e4m3 [E,2I,H], I = inner
+ *   gate_up_scales  fp32 [E, ceil(2I/128), ceil(H/128)] or NULL
+ *   down            payload or e4m3 [E,H,I]
+ *   down_scales     fp32 [E, ceil(H/128), ceil(I/128)]; NULL iff the other is
+ *   result          payload [T,H]
+ *   workspace       ep_expert_layer_workspace bytes, rewritten here: calls that
+ *                   share one must be ordered on the GPU
+ */
+#define EP_MAX_LAYER_ROUTES 1024
+
+/* 0 for an invalid layout or size. Host only. */
+size_t ep_expert_layer_workspace(const ep_layout_t* layout, int64_t inner);
+
+ep_status_t ep_expert_layer(const ep_layout_t* layout, const int64_t* topk_idx,
+                            const float* topk_weights, const void* tokens, const void* gate_up,
+                            const float* gate_up_scales, const void* down,
+                            const float* down_scales, void* result, int64_t inner,
+                            void* workspace, size_t workspace_bytes, hipStream_t stream);
 
 /* Copy the handle's status word (EP_STATUS_* bits) to *host_out. Waits for
  * `stream`; not for the hot path. host_out is a host pointer. The library's
