@@ -74,4 +74,36 @@ inline Kernel kernel_of(Product p, const Dims& d, int64_t N, int num_cus) {
   return Kernel::kTile128;
 }
 
+// The same for the product of 8-bit operands (ep_scaled.hip), measured in bf16 at
+// 128 experts, 2048 inputs and 1536 outputs unless another size is named.
+inline Kernel scaled_kernel_of(const Dims& d, int64_t N, int num_cus) {
+  const int64_t rows = most_rows(d) / d.E;
+  // up to 8 rows: 8 rows 67 us against 68 with the tiles below, 4 rows 64 against
+  // 69, one 41 against 46; 12 rows 75 against 71, 16 rows 97 against 73. One expert
+  // has no more rows than there are: 16 of 4096 x 4096 take 10 against 16
+  if (rows <= 8 || (d.E == 1 && rows <= 16)) return Kernel::kFewRows;
+  const int64_t tiles256 = (rows + 255) / 256 * ((N + 255) / 256) * d.E;
+  const int64_t tiles128 = (rows + 127) / 128 * ((N + 127) / 128) * d.E;
+  // 256 x 256 tiles from 105 rows: 112 rows 102 us against 113, 96 rows 99 against
+  // 92; from 41 where the contraction is deep (64 experts, 7168 x 4096: 63 rows 359
+  // against 363, 95 rows 374 against 388, 31 rows 331 against 330). They have to fill
+  // the CUs, or half of them where their rows would fill two tiles of 128 (8
+  // experts, 4096 x 4096: 256 rows 60 against 78, 128 rows 50 against 43).
+  if ((rows > 104 || (rows > 40 && d.H >= 4096)) &&
+      tiles256 >= (rows > 128 ? num_cus / 2 : num_cus)) {
+    // the weights past the caches while most experts have one row tile: 160 rows 112
+    // us against 120, 192 rows 117 against 127; 256 rows of 8 experts 62 against 60,
+    // 4096 rows of 8 (4096 x 28672) 4700 against 4040
+    return rows <= 192 ? Kernel::kTile256Once : Kernel::kTile256;
+  }
+  // 64 x 64 tiles where larger ones would leave CUs without work (one expert of 256
+  // rows, 4096 x 4096: 22 us against 31; 7 of 476 rows, 1040 x 776: 13.9 against
+  // 14.3), or would give each one tile of few rows (8 experts: 32 rows 33 against 39,
+  // 64 rows 36 against 40, but 128 rows 62 against 43)
+  if (tiles128 < num_cus || (rows <= 64 && tiles128 < 2 * num_cus)) return Kernel::kTile64;
+  // weights past the caches up to 104 rows: 24 rows 77 us against 84, 96 rows 92
+  // against 100, but 128 rows 134 against 132
+  return rows <= 104 ? Kernel::kTile128Once : Kernel::kTile128;
+}
+
 }  // namespace epmi

@@ -21,75 +21,121 @@ namespace {
 constexpr int kMaxRoutes = EP_MAX_LAYER_ROUTES;
 constexpr int kRowTile = 16;
 
-// What a block works on: expert number `index` among those that have a route, in
-// ascending order, and the routes of that expert, in ascending order too.
+// The routing table in LDS: the expert of each route, kNone without a valid one,
+// and a bit for each expert that has a route.
 struct Routes {
-  uint32_t has[kMaxExperts / 32];   // experts with a route
-  uint16_t of[kMaxRoutes];          // expert of each route, kNone without one
-  uint16_t rows[kMaxRoutes];        // the expert's routes
+  uint32_t has[kMaxExperts / 32];
+  uint16_t of[kMaxRoutes];
 };
 constexpr uint16_t kNone = 0xFFFF;
 static_assert(kMaxExperts / 32 == kWave, "a word a lane");
 
-struct Found {
-  int32_t active;   // experts with a route
-  int32_t expert;   // if index < active
-  int32_t rows;
+// What a wavefront keeps of it: the experts with a route, in ascending order.
+struct Active {
+  uint32_t word;     // this lane's 32 experts
+  int32_t before;    // experts with a route in the lanes below
+  int32_t all;
+
+  // Called by the whole block.
+  template <int THREADS>
+  __device__ static __forceinline__ Active of(const int64_t* __restrict__ topk_idx, int32_t n,
+                                              int32_t E, Routes& r) {
+    const int lane = lane_id();
+    if (threadIdx.x < kMaxExperts / 32) r.has[threadIdx.x] = 0;
+    __syncthreads();
+    for (int32_t s = threadIdx.x; s < n; s += THREADS) {
+      const int64_t id = topk_idx[s];
+      const bool valid = id >= 0 && id < E;
+      r.of[s] = valid ? (uint16_t)id : kNone;
+      if (valid) atomicOr(&r.has[id / 32], 1u << (id % 32));
+    }
+    __syncthreads();
+    Active a;
+    a.word = r.has[lane];
+    int32_t sum = __popc(a.word);
+    static_for<6>([&](auto i) {
+      const int32_t below = __shfl_up(sum, 1u << i, kWave);
+      if (lane >= (1 << i)) sum += below;
+    });
+    a.all = __builtin_amdgcn_readlane(sum, kWave - 1);
+    a.before = sum - __popc(a.word);
+    return a;
+  }
+
+  // Expert number `index` of them.
+  __device__ __forceinline__ int32_t expert(int32_t index) const {
+    const uint64_t at = wave_ballot(before <= index && index < before + __popc(word));
+    const int from = __builtin_ctzll(at);
+    uint32_t bits = (uint32_t)__builtin_amdgcn_readlane((int)word, from);
+    int32_t skip = index - __builtin_amdgcn_readlane(before, from);
+    while (skip-- > 0) bits &= bits - 1;
+    return from * 32 + __builtin_ctz(bits);
+  }
 };
 
-// Called by the whole block. Every wavefront writes all of r.rows, the same
-// values, and so needs no barrier to read them.
-template <int THREADS>
-__device__ __forceinline__ Found find_expert(const int64_t* __restrict__ topk_idx, int32_t n,
-                                             int32_t E, int32_t index, Routes& r) {
+// The expert's routes in ascending order: how many, and number first + i of them
+// in each lane i below 16 (and so in i + 16, i + 32, i + 48), as far as there are;
+// the last one beyond. `mine` is the wavefront's own.
+__device__ __forceinline__ int32_t routes_of(const Routes& r, int32_t n, int32_t expert,
+                                             int32_t first, uint16_t (&mine)[kRowTile],
+                                             int32_t& route) {
   const int lane = lane_id();
-  if (threadIdx.x < kMaxExperts / 32) r.has[threadIdx.x] = 0;
-  __syncthreads();
-  for (int32_t s = threadIdx.x; s < n; s += THREADS) {
-    const int64_t id = topk_idx[s];
-    const bool valid = id >= 0 && id < E;
-    r.of[s] = valid ? (uint16_t)id : kNone;
-    if (valid) atomicOr(&r.has[id / 32], 1u << (id % 32));
-  }
-  __syncthreads();
-  const uint32_t word = r.has[lane];
-  const int32_t mine = __popc(word);
-  int32_t sum = mine;
-  static_for<6>([&](auto i) {
-    const int32_t below = __shfl_up(sum, 1u << i, kWave);
-    if (lane >= (1 << i)) sum += below;
-  });
-  Found f;
-  f.active = __builtin_amdgcn_readlane(sum, kWave - 1);
-  f.expert = 0;
-  f.rows = 0;
-  if (index >= f.active) return f;
-  const uint64_t at = wave_ballot(sum - mine <= index && index < sum);
-  const int word_lane = __builtin_ctzll(at);
-  uint32_t bits = (uint32_t)__builtin_amdgcn_readlane((int)word, word_lane);
-  int32_t skip = index - __builtin_amdgcn_readlane(sum - mine, word_lane);
-  while (skip-- > 0) bits &= bits - 1;
-  f.expert = word_lane * 32 + __builtin_ctz(bits);
+  int32_t rows = 0;
+  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
   for (int32_t s0 = 0; s0 < n; s0 += kWave) {
     const int32_t s = s0 + lane;
-    const bool hit = s < n && r.of[s] == f.expert;
+    const bool hit = s < n && r.of[s] == expert;
     const uint64_t hits = wave_ballot(hit);
-    if (hit) r.rows[f.rows + __popcll(hits & ((1ull << lane) - 1))] = (uint16_t)s;
-    f.rows += __popcll(hits);
+    const int32_t at = rows + __popcll(hits & ((1ull << lane) - 1)) - first;
+    if (hit && at >= 0 && at < kRowTile) mine[at] = (uint16_t)s;
+    rows += __popcll(hits);
   }
   __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-  return f;
+  const int32_t last = rows - first < kRowTile ? rows - first - 1 : kRowTile - 1;
+  const int32_t i = lane & 15;
+  route = mine[i < last ? i : last];
+  return rows;
 }
 
-// A tile's columns: COLS / 2 of gate and the same of up (UP), or COLS of the
-// second product.
+// Four products of a route, written by one block and read by another, perhaps on
+// another XCD with an L2 of its own: stores and loads of agent scope, which go
+// through to the memory that the XCDs share. The fences that plain accesses would
+// need write back and invalidate a whole L2 for every block: with an
+// acquire-release add the second product took 802 us in place of 257 (batch of 16,
+// 256 experts of 7168 x 2048), with a fence in every thread 2442.
+__device__ __forceinline__ void put_product(float* to, f32x4 v) {
+  uint64_t* p = reinterpret_cast<uint64_t*>(to);
+  static_for<2>([&](auto i) {
+    const uint64_t bits = (uint64_t)__float_as_uint(v[2 * i.value]) |
+                          (uint64_t)__float_as_uint(v[2 * i.value + 1]) << 32;
+    __hip_atomic_store(p + i, bits, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+  });
+}
+__device__ __forceinline__ f32x4 get_product(const float* from) {
+  const uint64_t* p = reinterpret_cast<const uint64_t*>(from);
+  f32x4 v;
+  static_for<2>([&](auto i) {
+    const uint64_t bits = __hip_atomic_load(p + i, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    v[2 * i.value] = __uint_as_float((uint32_t)bits);
+    v[2 * i.value + 1] = __uint_as_float((uint32_t)(bits >> 32));
+  });
+  return v;
+}
+
+// A tile is up to 16 rows of an expert by COLS / 2 columns of gate and the same of
+// up (UP), or by COLS columns of the second product. The wavefronts take the steps
+// of k in turn and add their sums in LDS at the end, by when each has the first
+// loads of the block's next tile in flight. An expert's row tiles follow each
+// other in one block.
 template <int F, int DT, int COLS, int WAVES, bool UP>
 __global__ void __launch_bounds__(WAVES* kWave)
     layer_kernel(Dims d, LayerArgs a) {
   using S = Lines<F, DT, COLS>;
   constexpr int kThreads = WAVES * kWave, kHalf = COLS / 2;
-  __shared__ __align__(16) char mem[WAVES * S::kLds];
+  constexpr int kTileCols = UP ? kHalf : COLS, kQuads = kTileCols / 4;
+  extern __shared__ __align__(16) char mem[];      // WAVES * S::kLds
   __shared__ Routes routes;
+  __shared__ uint16_t row_lists[WAVES][kRowTile];
   __shared__ uint32_t last;
   const int32_t n = (int32_t)(d.T * d.K);
   const int32_t H = (int32_t)d.H, I = (int32_t)a.I;
@@ -97,73 +143,127 @@ __global__ void __launch_bounds__(WAVES* kWave)
   const int32_t cols_all = UP ? I : H;             // columns of either half, or all
   if constexpr (UP) {
     // the second product's counters
-    const int64_t all = (int64_t)gridDim.x * gridDim.y * kThreads;
-    for (int64_t i = ((int64_t)blockIdx.y * gridDim.x + blockIdx.x) * kThreads + threadIdx.x;
-         i < kLayerCounters; i += all)
+    for (int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x; i < kLayerCounters;
+         i += (int64_t)gridDim.x * kThreads)
       a.counters[i] = 0;
   }
-  const int32_t n0 = blockIdx.x * (UP ? kHalf : COLS);
-  const Found f = find_expert<kThreads>(a.topk_idx, n, d.E, blockIdx.y, routes);
+  const Active active = Active::of<kThreads>(a.topk_idx, n, d.E, routes);
   const int lane = lane_id(), i16 = lane & 15, q = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
   char* lds = mem + wave * S::kLds;
-  if (f.active == 0 && !UP && blockIdx.y == 0) {
-    // no route at all: the result is zeros
-    for (int32_t i = threadIdx.x; i < (int32_t)d.T * (COLS / 4); i += kThreads) {
-      const int32_t t = i / (COLS / 4), c = n0 + i % (COLS / 4) * 4;
-      if (c < H)
-        *reinterpret_cast<u32x2*>(static_cast<uint16_t*>(a.result) + (int64_t)t * H + c) =
-            u32x2{0, 0};
-    }
-  }
-  if ((int)blockIdx.y >= f.active) return;
+  const int32_t ct = (cols_all + kTileCols - 1) / kTileCols;
+  const int32_t tiles = active.all * ct;
 
-  const int64_t e = f.expert;
-  typename S::Source src;
-  const char* w = static_cast<const char*>(UP ? a.gate_up : a.down);
-  const int64_t w_row = (int64_t)K * S::kSize;
-  const int64_t first = e * (UP ? 2 * (int64_t)I : H);   // first row of the expert's matrix
-  src.w[0] = w + (first + n0) * w_row;
-  if constexpr (UP) {
-    src.cols[0] = src.cols[1] = I - n0 < kHalf ? I - n0 : kHalf;
-    src.w[1] = src.w[0] + I * w_row;
-  } else {
-    const int32_t left = H - n0;
-    src.cols[0] = left < kHalf ? left : kHalf;
-    src.cols[1] = left < COLS ? left - src.cols[0] : kHalf;
-    src.w[1] = src.w[0] + (src.cols[1] > 0 ? kHalf * w_row : 0);
+  // Every token's routes added up, ascending, in the columns from n0 on.
+  auto add_up = [&](int32_t n0) {
+    for (int32_t i = threadIdx.x; i < (int32_t)d.T * kQuads; i += kThreads) {
+      const int32_t t = i / kQuads, c = n0 + i % kQuads * 4;
+      if (c >= H) continue;
+      f32x4 sum = {0.f, 0.f, 0.f, 0.f};
+      bool any = false;
+      for (int32_t k = 0; k < d.K; ++k) {
+        const int32_t route = t * d.K + k;
+        if (routes.of[route] == kNone) continue;
+        const f32x4 y = get_product(a.y + (int64_t)route * H + c);
+        const float wk = a.topk_weights[route];
+        static_for<4>([&](auto j) {
+          sum[j.value] = any ? __builtin_fmaf(wk, y[j.value], sum[j.value]) : wk * y[j.value];
+        });
+        any = true;
+      }
+      *reinterpret_cast<u32x2*>(static_cast<uint16_t*>(a.result) + (int64_t)t * H + c) =
+          round_four<DT>(sum);
+    }
+  };
+  if constexpr (!UP) {
+    // no route at all: zeros
+    if (tiles == 0)
+      for (int32_t t = blockIdx.x; t < ct; t += gridDim.x) add_up(t * COLS);
   }
-  if constexpr (F == kWeights8) {
-    // the scales of the lane's four columns of each block of 16, which lie in one
-    const int32_t KB = pieces(K, kScaleBlock);
-    const int32_t NB = pieces(UP ? 2 * I : H, kScaleBlock);
-    const float* scales = UP ? a.gate_up_scales : a.down_scales;
-    static_for<S::kNF>([&](auto j) {
-      constexpr int half = j / (S::kNF / 2);
-      int32_t in = (j % (S::kNF / 2)) * 16 + q * 4;
-      in = in < src.cols[half] ? in : 0;
-      const int32_t c = n0 + (UP ? half * I : src.cols[half] > 0 ? half * kHalf : 0) + in;
-      src.w_scales[j] = scales + (e * NB + c / kScaleBlock) * KB;
-    });
-  }
+
+  struct Place {
+    typename S::Source src;
+    int32_t tile, n0;
+    int32_t first, rows;   // first row of the row tile, rows of the expert
+    int32_t route;         // of the lane's row
+  };
+  // Starts the loads of a tile: the weights', whose place the expert tells, before
+  // the expert's routes are looked up.
   S s;
-  for (int32_t r0 = 0; r0 < f.rows; r0 += kRowTile) {
-    const int32_t rows = f.rows - r0 < kRowTile ? f.rows - r0 : kRowTile;
-    const int32_t route = routes.rows[r0 + (i16 < rows ? i16 : rows - 1)];
-    src.x = UP ? static_cast<const char*>(a.tokens) + (int64_t)(route / d.K) * H * 2
-               : static_cast<const char*>(a.act) + (int64_t)route * I * 2;
-    s.first(src, wave, K);
+  auto start = [&](int32_t tile, int32_t first) {
+    Place p;
+    p.tile = tile;
+    p.first = first;
+    const int32_t e = active.expert(tile / ct);
+    p.n0 = tile % ct * kTileCols;
+    const char* w = static_cast<const char*>(UP ? a.gate_up : a.down);
+    const int64_t w_row = (int64_t)K * S::kSize;
+    const int64_t row = (int64_t)e * (UP ? 2 * (int64_t)I : H) + p.n0;
+    const int32_t left = cols_all - p.n0;
+    p.src.w[0] = w + row * w_row;
+    p.src.cols[0] = left < kHalf ? left : kHalf;
+    if constexpr (UP) {
+      p.src.cols[1] = p.src.cols[0];
+      p.src.w[1] = p.src.w[0] + I * w_row;
+    } else {
+      p.src.cols[1] = left < COLS ? left - p.src.cols[0] : kHalf;
+      p.src.w[1] = p.src.w[0] + (p.src.cols[1] > 0 ? kHalf * w_row : 0);
+    }
+    if constexpr (F == kWeights8) {
+      // the scales of the lane's four columns of each block of 16, which lie in one
+      const int32_t KB = pieces(K, kScaleBlock);
+      const int32_t NB = pieces(UP ? 2 * I : H, kScaleBlock);
+      const float* scales = (UP ? a.gate_up_scales : a.down_scales) + (int64_t)e * NB * KB;
+      static_for<S::kNF>([&](auto j) {
+        constexpr int half = j / (S::kNF / 2);
+        int32_t in = (j % (S::kNF / 2)) * 16 + q * 4;
+        in = in < p.src.cols[half] ? in : 0;
+        const int32_t c = p.n0 + (UP ? half * I : p.src.cols[half] > 0 ? half * kHalf : 0) + in;
+        p.src.w_scales[j] = scales + (int64_t)(c / kScaleBlock) * KB;
+      });
+    }
+    const bool mine = wave < K / S::kStep;
+    if (mine) s.template load_weights<false>(p.src, wave * S::kStep, K);
+    p.rows = routes_of(routes, n, e, first, row_lists[wave], p.route);
+    p.src.x = UP ? static_cast<const char*>(a.tokens) + (int64_t)(p.route / d.K) * H * 2
+                 : static_cast<const char*>(a.act) + (int64_t)p.route * I * 2;
+    if (mine) s.template load_x<false>(p.src, wave * S::kStep, K);
+    return p;
+  };
+  // UP = false: the tile whose products are on their way, its columns' counter not
+  // yet raised
+  int32_t pending = -1;
+  auto raise = [&]() {
+    if (threadIdx.x == 0)
+      last = pending >= 0 &&
+             __hip_atomic_fetch_add(&a.counters[pending], 1u, __ATOMIC_RELAXED,
+                                    __HIP_MEMORY_SCOPE_AGENT) == (uint32_t)active.all - 1;
+  };
+
+  Place next;
+  next.tile = blockIdx.x;
+  if (next.tile < tiles) next = start(next.tile, 0);
+  while (next.tile < tiles) {
+    const Place cur = next;
     f32x4 acc[S::kNF];
     static_for<S::kNF>([&](auto j) { acc[j] = f32x4{0.f, 0.f, 0.f, 0.f}; });
-    s.steps(lds, src, wave, WAVES, K, acc);
+    s.steps(lds, cur.src, wave, WAVES, K, acc);
+    // the last tile's products have been acknowledged (all loads are used up: this
+    // waits for nothing else)
+    if constexpr (!UP) asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+    const bool done = cur.first + kRowTile >= cur.rows;   // of this tile's expert
+    const int32_t rows = done ? cur.rows - cur.first : kRowTile;
+    next.tile = done ? cur.tile + (int32_t)gridDim.x : cur.tile;
+    if (next.tile < tiles) next = start(next.tile, done ? 0 : cur.first + kRowTile);
     S::put_sums(lds, acc);
     __syncthreads();
+    if constexpr (!UP) raise();
     // four columns of a row at a time
-    constexpr int kQuads = (UP ? kHalf : COLS) / 4;
     for (int i = threadIdx.x; i < kRowTile * kQuads; i += kThreads) {
       const int m = i / kQuads, c = i % kQuads * 4;
-      if (m < rows && n0 + c < cols_all) {
-        const int64_t at = (int64_t)routes.rows[r0 + m] * cols_all + n0 + c;
+      const int32_t route = __shfl(cur.route, m, kWave);
+      if (m < rows && cur.n0 + c < cols_all) {
+        const int64_t at = (int64_t)route * cols_all + cur.n0 + c;
         const f32x4 v = S::template sum_of<WAVES>(mem, m, c);
         if constexpr (UP) {
           const f32x4 u = S::template sum_of<WAVES>(mem, m, kHalf + c);
@@ -176,68 +276,77 @@ __global__ void __launch_bounds__(WAVES* kWave)
           // matrix instructions take it
           *reinterpret_cast<u32x2*>(static_cast<uint16_t*>(a.act) + at) = round_four<DT>(o);
         } else {
-          *reinterpret_cast<f32x4*>(a.y + at) = v;
+          put_product(a.y + at, v);
         }
       }
     }
     __syncthreads();
+    if constexpr (!UP) {
+      if (last) add_up(pending * COLS);
+      pending = done ? cur.tile % ct : -1;
+    }
   }
   if constexpr (!UP) {
-    // The last block of these columns adds up every token's routes, in ascending
-    // order whichever block that is.
-    __threadfence();
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
     __syncthreads();
-    if (threadIdx.x == 0)
-      last = atomicAdd(&a.counters[blockIdx.x], 1u) == (uint32_t)f.active - 1;
+    raise();
     __syncthreads();
-    if (!last) return;
-    __threadfence();
-    for (int32_t i = threadIdx.x; i < (int32_t)d.T * (COLS / 4); i += kThreads) {
-      const int32_t t = i / (COLS / 4), c = n0 + i % (COLS / 4) * 4;
-      if (c >= H) continue;
-      f32x4 sum = {0.f, 0.f, 0.f, 0.f};
-      bool any = false;
-      for (int32_t k = 0; k < d.K; ++k) {
-        const int32_t route = t * d.K + k;
-        if (routes.of[route] == kNone) continue;
-        const f32x4 y = *reinterpret_cast<const f32x4*>(a.y + (int64_t)route * H + c);
-        const float wk = a.topk_weights[route];
-        static_for<4>([&](auto j) {
-          sum[j.value] = any ? __builtin_fmaf(wk, y[j.value], sum[j.value]) : wk * y[j.value];
-        });
-        any = true;
-      }
-      *reinterpret_cast<u32x2*>(static_cast<uint16_t*>(a.result) + (int64_t)t * H + c) =
-          round_four<DT>(sum);
-    }
+    if (last) add_up(pending * COLS);
   }
 }
 
-template <int F, int DT>
-hipError_t launch_layer(const Dims& d, const LayerArgs& a, hipStream_t stream) {
-  constexpr int kCols = 64, kWaves = 4;
-  const int64_t n = d.T * d.K;
-  const uint32_t experts = (uint32_t)(n < d.E ? n : d.E);
-  layer_kernel<F, DT, kCols, kWaves, true>
-      <<<dim3((uint32_t)((a.I + kCols / 2 - 1) / (kCols / 2)), experts), dim3(kWaves * kWave), 0,
-         stream>>>(d, a);
-  const hipError_t e = hipGetLastError();
-  if (e != hipSuccess) return e;
-  layer_kernel<F, DT, kCols, kWaves, false>
-      <<<dim3((uint32_t)((d.H + kCols - 1) / kCols), experts), dim3(kWaves * kWave), 0, stream>>>(
+template <int F, int DT, bool UP, int COLS, int WAVES>
+hipError_t launch_product(const Dims& d, const LayerArgs& a, int64_t blocks, hipStream_t stream) {
+  constexpr int kTileCols = UP ? COLS / 2 : COLS;
+  const int64_t routes = d.T * d.K, cols = UP ? a.I : d.H;
+  // the most experts that the routes can reach
+  const int64_t tiles = (routes < d.E ? routes : d.E) * ((cols + kTileCols - 1) / kTileCols);
+  if (blocks > tiles) blocks = tiles;
+  layer_kernel<F, DT, COLS, WAVES, UP>
+      <<<dim3((uint32_t)blocks), dim3(WAVES * kWave), WAVES * Lines<F, DT, COLS>::kLds, stream>>>(
           d, a);
   return hipGetLastError();
 }
 
+// Columns of a tile and wavefronts that share its k; times of the two products
+// together, from one captured graph, weights out of HBM.
+//   16 bits, both products: 32 columns and eight wavefronts, two blocks a CU. Against
+//   64 columns and four wavefronts, four blocks: one token by top-2 of 8, 4096 x
+//   14336, 135 against 146 us (first product) and 126 against 146 (second); 16
+//   tokens by top-8 of 128, 2048 x 768, 139 and 145 against 149; 8 tokens of the
+//   first layer 380 and 407 against 405.
+//   8 bits, first product: 32 columns and four wavefronts, eight blocks: one token of
+//   the first layer 86 against 91, 16 tokens by top-8 of 256, 7168 x 2048, 699
+//   against 705 (64 tokens 1556 against 1544).
+//   8 bits, second product: 64 columns and four wavefronts, four blocks (with 32 and
+//   eight the 16 tokens take 782 against 703, their 16 steps of k being two a
+//   wavefront), but 32 and eight where tiles of 64 leave CUs without work: one token
+//   of the first layer 68 against 86.
+template <int F, int DT>
+hipError_t launch_layer(const Dims& d, const LayerArgs& a, int num_cus, hipStream_t stream) {
+  const int64_t cus = num_cus, routes = d.T * d.K;
+  if constexpr (F == kPayload) {
+    const hipError_t e = launch_product<F, DT, true, 32, 8>(d, a, 2 * cus, stream);
+    return e != hipSuccess ? e : launch_product<F, DT, false, 32, 8>(d, a, 2 * cus, stream);
+  } else {
+    const hipError_t e = launch_product<F, DT, true, 32, 4>(d, a, 8 * cus, stream);
+    if (e != hipSuccess) return e;
+    if ((routes < d.E ? routes : d.E) * ((d.H + 63) / 64) < cus)
+      return launch_product<F, DT, false, 32, 8>(d, a, 2 * cus, stream);
+    return launch_product<F, DT, false, 64, 4>(d, a, 4 * cus, stream);
+  }
+}
+
 }  // namespace
 
-hipError_t launch_expert_layer(const Dims& d, const LayerArgs& a, int, hipStream_t stream) {
+hipError_t launch_expert_layer(const Dims& d, const LayerArgs& a, int num_cus,
+                               hipStream_t stream) {
   const bool eight = a.gate_up_scales != nullptr;
   if (d.dtype == EP_DTYPE_FP16)
-    return eight ? launch_layer<kWeights8, EP_DTYPE_FP16>(d, a, stream)
-                 : launch_layer<kPayload, EP_DTYPE_FP16>(d, a, stream);
-  return eight ? launch_layer<kWeights8, EP_DTYPE_BF16>(d, a, stream)
-               : launch_layer<kPayload, EP_DTYPE_BF16>(d, a, stream);
+    return eight ? launch_layer<kWeights8, EP_DTYPE_FP16>(d, a, num_cus, stream)
+                 : launch_layer<kPayload, EP_DTYPE_FP16>(d, a, num_cus, stream);
+  return eight ? launch_layer<kWeights8, EP_DTYPE_BF16>(d, a, num_cus, stream)
+               : launch_layer<kPayload, EP_DTYPE_BF16>(d, a, num_cus, stream);
 }
 
 }  // namespace epmi

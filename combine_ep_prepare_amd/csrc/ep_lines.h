@@ -123,7 +123,7 @@ struct Lines {
   // (PART) a lane whose bytes are not there reads the rows' start and takes it
   // out again, of the weights and of x, whatever that holds.
   template <bool PART>
-  __device__ __forceinline__ void load(const Source& s, int32_t k0, int32_t K) {
+  __device__ __forceinline__ void load_weights(const Source& s, int32_t k0, int32_t K) {
     const int lane = lane_id();
     const uint32_t w_row = (uint32_t)K * kSize;
     const int chunk = (lane & 7) ^ (lane >> 3);
@@ -135,6 +135,9 @@ struct Lines {
       w[j] = __builtin_nontemporal_load(reinterpret_cast<const row16_t*>(column + at));
       if constexpr (PART) w[j] = in ? w[j] : row16_t{0, 0, 0, 0};
     });
+  }
+  template <bool PART>
+  __device__ __forceinline__ void load_x(const Source& s, int32_t k0, int32_t K) {
     static_for<kX>([&](auto p) {
       const int32_t k = k0 + input(p);
       const bool have = !PART || k < K;
@@ -146,6 +149,11 @@ struct Lines {
       static_for<kScales>([&](auto i) { scale[i] = s.w_scales[i][block]; });
       if constexpr (F == kScaled) x_scale = s.x_scales[block];
     }
+  }
+  template <bool PART>
+  __device__ __forceinline__ void load(const Source& s, int32_t k0, int32_t K) {
+    load_weights<PART>(s, k0, K);
+    load_x<PART>(s, k0, K);
   }
 
   // The loaded weights into the wavefront's LDS. Its lanes write and read it in

@@ -246,8 +246,9 @@ __global__ void __launch_bounds__(kSumThreads)
   }
 }
 
-// Wavefronts to a row and vectors to a lane.
-template <typename F>
+// Wavefronts to a row and vectors to a lane; V is at most EP_MAX_NORM_FEATURES
+// values.
+template <int DT, typename F>
 hipError_t with_row(int64_t V, F&& f) {
   using std::integral_constant;
   if (V <= 64) return f(integral_constant<int, 1>{}, integral_constant<int, 1>{});
@@ -255,8 +256,10 @@ hipError_t with_row(int64_t V, F&& f) {
   if (V <= 256) return f(integral_constant<int, 1>{}, integral_constant<int, 4>{});
   if (V <= 512) return f(integral_constant<int, 4>{}, integral_constant<int, 2>{});
   if (V <= 1024) return f(integral_constant<int, 4>{}, integral_constant<int, 4>{});
-  if (V <= 2048) return f(integral_constant<int, 16>{}, integral_constant<int, 2>{});
-  return f(integral_constant<int, 16>{}, integral_constant<int, 4>{});
+  if constexpr (DT == EP_DTYPE_FP32) {
+    if (V > 2048) return f(integral_constant<int, 16>{}, integral_constant<int, 4>{});
+  }
+  return f(integral_constant<int, 16>{}, integral_constant<int, 2>{});
 }
 
 // Blocks of the backward pass: each writes its part of the weight gradient.
@@ -270,7 +273,7 @@ int64_t bwd_blocks(const Dims& d, int rows) {
 
 hipError_t launch_rms_norm(const Dims& d, const NormArgs& a, int, hipStream_t stream) {
   return with_payload(d.dtype, [&](auto dt) {
-    return with_row(d.V, [&](auto waves, auto vpt) {
+    return with_row<decltype(dt)::value>(d.V, [&](auto waves, auto vpt) {
       constexpr int W = decltype(waves)::value;
       const int64_t blocks = (d.T + rows_of_block(W) - 1) / rows_of_block(W);
       // a grid has less than 2^32 threads in one direction: T < 2^31 rows of
@@ -306,10 +309,12 @@ hipError_t launch_rms_norm(const Dims& d, const NormArgs& a, int, hipStream_t st
 
 int64_t norm_bwd_partials(const Dims& d) {
   int64_t n = 0;
-  (void)with_row(d.V, [&](auto waves, auto) {
-    constexpr int R = rows_of_block(decltype(waves)::value);
-    n = bwd_blocks(d, R) * R;
-    return hipSuccess;
+  (void)with_payload(d.dtype, [&](auto dt) {
+    return with_row<decltype(dt)::value>(d.V, [&](auto waves, auto) {
+      constexpr int R = rows_of_block(decltype(waves)::value);
+      n = bwd_blocks(d, R) * R;
+      return hipSuccess;
+    });
   });
   return n;
 }
@@ -317,7 +322,7 @@ int64_t norm_bwd_partials(const Dims& d) {
 hipError_t launch_rms_norm_bwd(const Dims& d, const NormBwdArgs& a, int, hipStream_t stream) {
   return with_payload(d.dtype, [&](auto dt) {
     constexpr int DT = decltype(dt)::value;
-    hipError_t e = with_row(d.V, [&](auto waves, auto vpt) {
+    hipError_t e = with_row<DT>(d.V, [&](auto waves, auto vpt) {
       constexpr int W = decltype(waves)::value;
       rms_norm_bwd_kernel<DT, W, decltype(vpt)::value>
           <<<dim3((uint32_t)bwd_blocks(d, rows_of_block(W))), dim3(threads_of_block(W)), 0,

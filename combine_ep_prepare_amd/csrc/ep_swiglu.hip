@@ -118,10 +118,10 @@ __global__ void __launch_bounds__(kThreads)
   const int64_t live = hh.total < d.cap ? hh.total : d.cap;
   const int64_t rows = d.zero_tail ? d.cap : live;
   const int32_t V = (int32_t)d.V, S = (int32_t)EP_SCALE_COLUMNS(d.H);
+  const int32_t B = (V + kLanes - 1) / kLanes;   // blocks of a row
   const int32_t group = threadIdx.x / kLanes, lane = threadIdx.x % kLanes;
-  // S places a row: those past its values hold zeros alone
-  const int32_t row_first = group / S, b_first = group % S;
-  const int32_t row_by = kGroups / S, b_by = kGroups % S;
+  const int32_t row_first = group / B, b_first = group % B;
+  const int32_t row_by = kGroups / B, b_by = kGroups % B;
   for (int64_t r0 = (int64_t)blockIdx.x * step_rows; r0 < rows;
        r0 += (int64_t)gridDim.x * step_rows) {
     const int64_t r1 = r0 + step_rows < rows ? r0 + step_rows : rows;
@@ -131,8 +131,8 @@ __global__ void __launch_bounds__(kThreads)
     while (r < r1) {
       int64_t next_r = r + row_by;
       int32_t next_b = b + b_by;
-      if (next_b >= S) {
-        next_b -= S;
+      if (next_b >= B) {
+        next_b -= B;
         ++next_r;
       }
       const int32_t next_source = next_r < r1 && next_r < live ? hv.row_src[next_r] : -1;
@@ -140,7 +140,7 @@ __global__ void __launch_bounds__(kThreads)
       const bool in = v < V;
       uint32_t q[N / 4] = {};
       float scale = 0.f;
-      if (source >= 0 && b * kLanes < V) {
+      if (source >= 0) {
         row16_t gv = {0, 0, 0, 0}, uv = {0, 0, 0, 0};
         if (in) {
           gv = __builtin_nontemporal_load(gate_up + r * 2 * V + v);
@@ -165,7 +165,9 @@ __global__ void __launch_bounds__(kThreads)
           uint32_t* to = reinterpret_cast<uint32_t*>(out_q + r * d.H) + (int64_t)v * (N / 4);
           static_for<N / 4>([&](auto j) { to[j] = q[j]; });
         }
-        if (lane == 0) out_scales[r * S + b] = scale;
+        // with the last block, the columns past it too, fewer than eight
+        if (lane == 0 || (b == B - 1 && lane < S - b))
+          out_scales[r * S + b + lane] = lane == 0 ? scale : 0.f;
       }
       r = next_r;
       b = next_b;

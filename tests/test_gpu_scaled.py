@@ -266,3 +266,15 @@ def test_gradients_are_refused():
     y = epa.rms_norm(x, w, 1e-6)
     with pytest.raises(RuntimeError, match="second derivative"):
         torch.autograd.grad(y.sum(), x, create_graph=True)
+
+
+@pytest.mark.parametrize("kind,T,K,E,A,H,N", [
+    ("any", 140, 2, 40, 1, 528, 520), ("steep", 900, 2, 16, 4, 272, 1160),   # 64 x 64 tiles
+    ("any", 1200, 2, 64, 1, 272, 1032), ("masked", 1500, 4, 64, 8, 656, 1048),   # 128 x 128
+    ("any", 6000, 2, 96, 1, 272, 1032), ("steep", 9000, 2, 64, 4, 400, 1288),   # 256 x 256
+    ("any", 3300, 2, 8, 16, 144, 4104), ("one", 700, 1, 2, 1, 272, 16392),
+    ("any", 1700, 2, 64, 1, 4112, 1032)])
+def test_linear_tiles(kind, T, K, E, A, H, N):
+    """Every tile size, of whole numbers: ragged rows, features, segments and last
+    blocks, tiles with part of their rows, experts without any."""
+    linear_case(Case(kind, T, K, E, A, "bf16", seed=T), H, N, whole=True)
