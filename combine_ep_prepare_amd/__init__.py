@@ -228,7 +228,8 @@ def handle_maps(layout: Layout, handle: torch.Tensor) -> dict:
 # The checks below run for every tensor of every call, and the small calls of
 # decoding take about as long on the host as on the GPU: plain ints for
 # pointers (the argument types convert them), one query each for a tensor's
-# device and the current one.
+# device and the current one, the latter without torch.cuda's check that there
+# is a context: a tensor on a GPU has one.
 
 def _ptr(t: Optional[torch.Tensor]) -> Optional[int]:
     return None if t is None else t.data_ptr()
@@ -236,7 +237,7 @@ def _ptr(t: Optional[torch.Tensor]) -> Optional[int]:
 
 def _stream(stream) -> int:
     if stream is None:
-        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+        return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
     return stream.cuda_stream
 
 
@@ -250,13 +251,32 @@ def _need(t: Optional[torch.Tensor], name: str, dtype, shape=None, allow_none=Fa
     device = t.get_device()
     if device < 0 or not t.is_cuda:
         raise ValueError(f"{name} must be a GPU tensor")
-    if device != torch.cuda.current_device():
+    if device != torch._C._cuda_getDevice():
         raise ValueError(f"{name} is on {t.device}; the library runs on the current device "
                          f"cuda:{torch.cuda.current_device()}")
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
     if shape is not None and t.shape != shape:
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+
+
+def _need_all(required, optional=()):
+    """_need for several (tensor, name, dtype, shape), those of `optional` perhaps
+    None: one query for the current device, and what is amiss said by _need."""
+    current = torch._C._cuda_getDevice() if torch.cuda.is_initialized() else 0
+    for t, name, dtype, shape in required:
+        if (t is None or t.dtype is not dtype or t.get_device() != current
+                or not t.is_contiguous() or t.shape != shape):
+            _need(t, name, dtype, shape)
+    for t, name, dtype, shape in optional:
+        if t is not None and (t.dtype is not dtype or t.get_device() != current
+                              or not t.is_contiguous() or t.shape != shape):
+            _need(t, name, dtype, shape)
+
+
+def _both(name_a: str, a, name_b: str, b):
+    if (a is None) != (b is None):
+        raise ValueError(f"{name_a} and {name_b} go together")
 
 
 def _out_features(weight: torch.Tensor) -> int:
@@ -471,15 +491,16 @@ def rms_norm(layout: Layout, x: torch.Tensor, weight: torch.Tensor, eps: float,
     """The norm of x [T,H] (with a residual: of sum_out = x + residual) times
     weight [H], into out [T,H], or in 8 bits into out_q with out_scales
     [T, scale_columns(H)], or both."""
-    rows, dtype = (layout.T, layout.H), layout.payload_dtype
-    _need(x, "x", dtype, rows)
-    _need(weight, "weight", dtype, (layout.H,))
-    _need(out, "out", dtype, rows, allow_none=out_q is not None)
-    _need(out_q, "out_q", E4M3, rows, allow_none=True)
-    _need(out_scales, "out_scales", torch.float32, (layout.T, scale_columns(layout.H)),
-          allow_none=out_q is None)
-    _need(residual, "residual", dtype, rows, allow_none=sum_out is None)
-    _need(sum_out, "sum_out", dtype, rows, allow_none=residual is None)
+    T, H, dtype = layout.num_tokens, layout.hidden, layout.payload_dtype
+    if out is None and out_q is None:
+        raise ValueError("out or out_q is required")
+    _both("out_q", out_q, "out_scales", out_scales)
+    _both("residual", residual, "sum_out", sum_out)
+    rows = (T, H)
+    _need_all(((x, "x", dtype, rows), (weight, "weight", dtype, (H,))),
+              ((out, "out", dtype, rows), (out_q, "out_q", E4M3, rows),
+               (out_scales, "out_scales", torch.float32, (T, scale_columns(H))),
+               (residual, "residual", dtype, rows), (sum_out, "sum_out", dtype, rows)))
     _check(lib.ep_rms_norm(C.byref(layout), _ptr(x), _ptr(residual), _ptr(weight), eps,
                            _ptr(sum_out), _ptr(out), _ptr(out_q), _ptr(out_scales),
                            _stream(stream)), "ep_rms_norm")
@@ -501,14 +522,13 @@ def rms_norm_bwd(layout: Layout, grad: torch.Tensor, x: torch.Tensor, weight: to
     (x, or sum_out with a residual) and the weight; grad_sum is a gradient of
     sum_out that is added to the first. A grad_weight that is None is skipped, and
     needs no workspace."""
-    rows, dtype = (layout.T, layout.H), layout.payload_dtype
-    _need(grad, "grad", dtype, rows)
-    _need(x, "x", dtype, rows)
-    _need(weight, "weight", dtype, (layout.H,))
-    _need(grad_x, "grad_x", dtype, rows)
-    _need(grad_weight, "grad_weight", dtype, (layout.H,), allow_none=True)
-    _need(workspace, "workspace", torch.uint8, allow_none=grad_weight is None)
-    _need(grad_sum, "grad_sum", dtype, rows, allow_none=True)
+    H, dtype = layout.hidden, layout.payload_dtype
+    rows = (layout.num_tokens, H)
+    if grad_weight is not None:
+        _need(workspace, "workspace", torch.uint8)
+    _need_all(((grad, "grad", dtype, rows), (x, "x", dtype, rows),
+               (weight, "weight", dtype, (H,)), (grad_x, "grad_x", dtype, rows)),
+              ((grad_weight, "grad_weight", dtype, (H,)), (grad_sum, "grad_sum", dtype, rows)))
     _check(lib.ep_rms_norm_bwd(C.byref(layout), _ptr(grad), _ptr(grad_sum), _ptr(x),
                                _ptr(weight), eps, _ptr(grad_x), _ptr(grad_weight),
                                _ptr(workspace), 0 if workspace is None else workspace.numel(),
@@ -519,10 +539,11 @@ def swiglu_scaled(layout: Layout, handle: torch.Tensor, gate_up: torch.Tensor,
                   out_q: torch.Tensor, out_scales: torch.Tensor, stream=None):
     """``swiglu`` with its result in 8 bits: out_q [cap,H] and out_scales
     [cap, scale_columns(H)]."""
+    cap, H = layout.recv_capacity, layout.hidden
     _need(handle, "handle", torch.uint8)
-    _need(gate_up, "gate_up", layout.payload_dtype, (layout.cap, 2 * layout.H))
-    _need(out_q, "out_q", E4M3, (layout.cap, layout.H))
-    _need(out_scales, "out_scales", torch.float32, (layout.cap, scale_columns(layout.H)))
+    _need_all(((gate_up, "gate_up", layout.payload_dtype, (cap, 2 * H)),
+               (out_q, "out_q", E4M3, (cap, H)),
+               (out_scales, "out_scales", torch.float32, (cap, scale_columns(H)))))
     _check(lib.ep_swiglu_scaled(C.byref(layout), _ptr(handle), handle.numel(), _ptr(gate_up),
                                 _ptr(out_q), _ptr(out_scales), _stream(stream)),
            "ep_swiglu_scaled")
@@ -534,14 +555,14 @@ def grouped_linear_scaled(layout: Layout, handle: torch.Tensor, x: torch.Tensor,
     """``grouped_linear`` of 8-bit operands: x [cap,H] with x_scales
     [cap, scale_columns(H)], weight [E,N,H] with weight_scales
     [E, ceil(N/128), ceil(H/128)]; out [cap,N] of the layout's payload type."""
-    N = _out_features(weight)
+    N, E, H, cap = _out_features(weight), layout.num_experts, layout.hidden, layout.recv_capacity
     _need(handle, "handle", torch.uint8)
-    _need(x, "x", E4M3, (layout.cap, layout.H))
-    _need(x_scales, "x_scales", torch.float32, (layout.cap, scale_columns(layout.H)))
-    _need(weight, "weight", E4M3, (layout.E, N, layout.H))
-    _need(weight_scales, "weight_scales", torch.float32,
-          (layout.E, _scale_blocks(N), _scale_blocks(layout.H)))
-    _need(out, "out", layout.payload_dtype, (layout.cap, N))
+    _need_all(((x, "x", E4M3, (cap, H)),
+               (x_scales, "x_scales", torch.float32, (cap, scale_columns(H))),
+               (weight, "weight", E4M3, (E, N, H)),
+               (weight_scales, "weight_scales", torch.float32,
+                (E, _scale_blocks(N), _scale_blocks(H))),
+               (out, "out", layout.payload_dtype, (cap, N))))
     _check(lib.ep_grouped_linear_scaled(C.byref(layout), _ptr(handle), handle.numel(), _ptr(x),
                                         _ptr(x_scales), _ptr(weight), _ptr(weight_scales),
                                         _ptr(out), N, _stream(stream)),
@@ -568,19 +589,20 @@ def expert_layer(layout: Layout, topk_idx: torch.Tensor, topk_weights: torch.Ten
     payload type, or in 8 bits with both scales."""
     if down.dim() != 3:
         raise ValueError(f"down must have shape (E, H, I), got {tuple(down.shape)}")
-    E, H, inner, dtype = layout.E, layout.H, down.shape[2], layout.payload_dtype
-    eight = gate_up_scales is not None or down_scales is not None
-    _need(topk_idx, "topk_idx", torch.int64, (layout.T, layout.K))
-    _need(topk_weights, "topk_weights", torch.float32, (layout.T, layout.K))
-    _need(tokens, "tokens", dtype, (layout.T, H))
-    _need(gate_up, "gate_up", E4M3 if eight else dtype, (E, 2 * inner, H))
-    _need(down, "down", E4M3 if eight else dtype, (E, H, inner))
-    _need(gate_up_scales, "gate_up_scales", torch.float32,
-          (E, _scale_blocks(2 * inner), _scale_blocks(H)), allow_none=not eight)
-    _need(down_scales, "down_scales", torch.float32,
-          (E, _scale_blocks(H), _scale_blocks(inner)), allow_none=not eight)
-    _need(result, "result", dtype, (layout.T, H))
+    T, K, E, H = layout.num_tokens, layout.topk, layout.num_experts, layout.hidden
+    inner, dtype = down.shape[2], layout.payload_dtype
+    _both("gate_up_scales", gate_up_scales, "down_scales", down_scales)
+    weights = dtype if gate_up_scales is None else E4M3
     _need(workspace, "workspace", torch.uint8)
+    _need_all(((topk_idx, "topk_idx", torch.int64, (T, K)),
+               (topk_weights, "topk_weights", torch.float32, (T, K)),
+               (tokens, "tokens", dtype, (T, H)),
+               (gate_up, "gate_up", weights, (E, 2 * inner, H)),
+               (down, "down", weights, (E, H, inner)), (result, "result", dtype, (T, H))),
+              ((gate_up_scales, "gate_up_scales", torch.float32,
+                (E, _scale_blocks(2 * inner), _scale_blocks(H))),
+               (down_scales, "down_scales", torch.float32,
+                (E, _scale_blocks(H), _scale_blocks(inner)))))
     _check(lib.ep_expert_layer(C.byref(layout), _ptr(topk_idx), _ptr(topk_weights),
                                _ptr(tokens), _ptr(gate_up), _ptr(gate_up_scales), _ptr(down),
                                _ptr(down_scales), _ptr(result), inner, _ptr(workspace),

@@ -12,7 +12,7 @@
 //
 // Both are bound by HBM traffic. A row is read once and stays in registers
 // between its sums and its results: a wavefront holds rows of up to 256 16-byte
-// vectors, a block of four or of sixteen wavefronts longer ones. Sums are fp32.
+// vectors, a block of four to sixteen wavefronts longer ones. Sums are fp32.
 
 #include "ep_experts.h"
 #include "ep_gate.h"
@@ -74,6 +74,12 @@ __global__ void __launch_bounds__(threads_of_block(WAVES))
     s[i] = row16_t{0, 0, 0, 0};
     if (v < V) s[i] = __builtin_nontemporal_load(x + v);
   });
+  // asked for with the rows: the stores below keep later loads behind them
+  static_for<VPT>([&](auto i) {
+    const int v = i * (WAVES * kWave) + t;
+    w[i] = row16_t{0, 0, 0, 0};
+    if (v < V) w[i] = weight[v];
+  });
   if (a.residual) {
     row16_t b[VPT];
     static_for<VPT>([&](auto i) {
@@ -91,11 +97,6 @@ __global__ void __launch_bounds__(threads_of_block(WAVES))
       if (v < V) store_stream16(static_cast<row16_t*>(a.sum) + row * V + v, s[i]);
     });
   }
-  static_for<VPT>([&](auto i) {
-    const int v = i * (WAVES * kWave) + t;
-    w[i] = row16_t{0, 0, 0, 0};
-    if (v < V) w[i] = weight[v];
-  });
   float ss = 0.f, none = 0.f;
   static_for<VPT>([&](auto i) {
     static_for<N>([&](auto j) {
@@ -117,17 +118,12 @@ __global__ void __launch_bounds__(threads_of_block(WAVES))
     }
     if (a.out_q) {
       // lanes past the row hold zeros
-      float amax = 0.f;
-      static_for<N>([&](auto j) { amax = __builtin_fmaxf(amax, finite_magnitude(y[j])); });
-      const BlockScale b = block_scale(group_max<kLanes>(amax));
-      static_for<N>([&](auto j) { y[j] *= b.by; });
+      uint32_t q[N / 4];
+      const float scale = quantise<kLanes>(y, q);
       const int64_t S = EP_SCALE_COLUMNS(d.H);
       if (v < V) {
-        uint32_t* q = reinterpret_cast<uint32_t*>(a.out_q + row * d.H) + (int64_t)v * (N / 4);
-        static_for<N / 4>([&](auto j) {
-          q[j] = to_e4m3(y[4 * j], y[4 * j + 1], y[4 * j + 2], y[4 * j + 3]);
-        });
-        if (v % kLanes == 0) a.out_scales[row * S + v / kLanes] = b.scale;
+        store_bytes(a.out_q + row * d.H + (int64_t)v * N, q);
+        if (v % kLanes == 0) a.out_scales[row * S + v / kLanes] = scale;
       }
     }
   });
@@ -197,11 +193,26 @@ __global__ void __launch_bounds__(threads_of_block(WAVES))
     });
   }
   if (!a.grad_weight) return;
-  // also where the block had no row: every partial row is read
+  // one part a block, also where it had no row: every part is read
+  if constexpr (WAVES == 1) {
+    __shared__ float others[kRows - 1][VPT * N][kWave];
+    const int wave = threadIdx.x / kWave;
+    if (wave > 0)
+      static_for<VPT>([&](auto i) {
+        static_for<N>([&](auto j) { others[wave - 1][i * N + j][t] = dw[i][j]; });
+      });
+    __syncthreads();
+    if (wave > 0) return;
+    static_for<kRows - 1>([&](auto w) {
+      static_for<VPT>([&](auto i) {
+        static_for<N>([&](auto j) { dw[i][j] += others[w][i * N + j][t]; });
+      });
+    });
+  }
   static_for<VPT>([&](auto i) {
     const int v = i * (WAVES * kWave) + t;
     if (v < V) {
-      float* to = a.partial + slot * d.H + (int64_t)v * N;
+      float* to = a.partial + (int64_t)blockIdx.x * d.H + (int64_t)v * N;
       static_for<N / 4>([&](auto j) {
         reinterpret_cast<row16_t*>(to)[j] =
             row16_t{__float_as_uint(dw[i][4 * j]), __float_as_uint(dw[i][4 * j + 1]),
@@ -248,22 +259,31 @@ __global__ void __launch_bounds__(kSumThreads)
 
 // Wavefronts to a row and vectors to a lane; V is at most EP_MAX_NORM_FEATURES
 // values.
-template <int DT, typename F>
+template <int DT, bool BWD, typename F>
 hipError_t with_row(int64_t V, F&& f) {
   using std::integral_constant;
   if (V <= 64) return f(integral_constant<int, 1>{}, integral_constant<int, 1>{});
   if (V <= 128) return f(integral_constant<int, 1>{}, integral_constant<int, 2>{});
   if (V <= 256) return f(integral_constant<int, 1>{}, integral_constant<int, 4>{});
   if (V <= 512) return f(integral_constant<int, 4>{}, integral_constant<int, 2>{});
-  if (V <= 1024) return f(integral_constant<int, 4>{}, integral_constant<int, 4>{});
+  if (V <= 1024) {
+    // eight wavefronts, 32768 rows of 7168 bf16 values with a residual, in 8 bits: 268
+    // us against 276 with four; backward, where the weight's sums are a lane's too, four
+    if constexpr (!BWD) return f(integral_constant<int, 8>{}, integral_constant<int, 2>{});
+    return f(integral_constant<int, 4>{}, integral_constant<int, 4>{});
+  }
   if constexpr (DT == EP_DTYPE_FP32) {
     if (V > 2048) return f(integral_constant<int, 16>{}, integral_constant<int, 4>{});
   }
   return f(integral_constant<int, 16>{}, integral_constant<int, 2>{});
 }
 
-// Blocks of the backward pass: each writes its part of the weight gradient.
-constexpr int64_t kBwdBlocks = 1024;
+// Blocks of the backward pass, two a CU: each writes its part of the weight
+// gradient. 16384 rows of 4096 bf16 values with a gradient of the sum: 98 us,
+// against 103 with 768, 111 with 1024 (whose parts are 17 MB more to write and
+// read) and 115 with 2048; with the next row's loads ahead of this one's sums 99
+// (106 with 256).
+constexpr int64_t kBwdBlocks = 512;
 int64_t bwd_blocks(const Dims& d, int rows) {
   const int64_t blocks = (d.T + rows - 1) / rows;
   return blocks < 1 ? 1 : blocks < kBwdBlocks ? blocks : kBwdBlocks;
@@ -273,7 +293,7 @@ int64_t bwd_blocks(const Dims& d, int rows) {
 
 hipError_t launch_rms_norm(const Dims& d, const NormArgs& a, int, hipStream_t stream) {
   return with_payload(d.dtype, [&](auto dt) {
-    return with_row<decltype(dt)::value>(d.V, [&](auto waves, auto vpt) {
+    return with_row<decltype(dt)::value, false>(d.V, [&](auto waves, auto vpt) {
       constexpr int W = decltype(waves)::value;
       const int64_t blocks = (d.T + rows_of_block(W) - 1) / rows_of_block(W);
       // a grid has less than 2^32 threads in one direction: T < 2^31 rows of
@@ -310,9 +330,8 @@ hipError_t launch_rms_norm(const Dims& d, const NormArgs& a, int, hipStream_t st
 int64_t norm_bwd_partials(const Dims& d) {
   int64_t n = 0;
   (void)with_payload(d.dtype, [&](auto dt) {
-    return with_row<decltype(dt)::value>(d.V, [&](auto waves, auto) {
-      constexpr int R = rows_of_block(decltype(waves)::value);
-      n = bwd_blocks(d, R) * R;
+    return with_row<decltype(dt)::value, true>(d.V, [&](auto waves, auto) {
+      n = bwd_blocks(d, rows_of_block(decltype(waves)::value));
       return hipSuccess;
     });
   });
@@ -322,7 +341,7 @@ int64_t norm_bwd_partials(const Dims& d) {
 hipError_t launch_rms_norm_bwd(const Dims& d, const NormBwdArgs& a, int, hipStream_t stream) {
   return with_payload(d.dtype, [&](auto dt) {
     constexpr int DT = decltype(dt)::value;
-    hipError_t e = with_row<DT>(d.V, [&](auto waves, auto vpt) {
+    hipError_t e = with_row<DT, true>(d.V, [&](auto waves, auto vpt) {
       constexpr int W = decltype(waves)::value;
       rms_norm_bwd_kernel<DT, W, decltype(vpt)::value>
           <<<dim3((uint32_t)bwd_blocks(d, rows_of_block(W))), dim3(threads_of_block(W)), 0,

@@ -9,11 +9,6 @@ namespace epmi {
 
 namespace {
 
-__device__ __forceinline__ float finite_magnitude(float v) {
-  const float m = __builtin_fabsf(v);
-  return m < __builtin_inff() ? m : 0.f;   // false for a NaN too
-}
-
 // The largest of m over aligned groups of LANES lanes (a power of two up to 32),
 // in every lane of the group.
 template <int LANES>
@@ -35,15 +30,51 @@ __device__ __forceinline__ BlockScale block_scale(float amax) {
   return BlockScale{m / kE4m3Max, kE4m3Max / m};
 }
 
-// Four values to e4m3, to nearest, ties to even. An infinity times `by` stays
-// one and a NaN a NaN; both become e4m3's NaN (0x7F, which the conversion may
-// give with either sign).
-__device__ __forceinline__ uint32_t to_e4m3(float a, float b, float c, float d) {
-  // an infinity would be cut off at 448, were the conversion to saturate
-  auto nan = [](float v) { return __builtin_fabsf(v) < __builtin_inff() ? v : __builtin_nanf(""); };
-  int q = __builtin_amdgcn_cvt_pk_fp8_f32(nan(a), nan(b), 0, false);
-  q = __builtin_amdgcn_cvt_pk_fp8_f32(nan(c), nan(d), q, true);
-  return (uint32_t)q;
+// NV values of a block, of which a group of LANES lanes holds NV each, to e4m3, four
+// to a word; returns the scale. Called by whole groups. Values that are not finite
+// are looked for once, by the wavefront, and taken apart only where there are any:
+// apart from that a value costs its maximum, half a comparison, a product and half a
+// conversion.
+template <int LANES, int NV>
+__device__ __forceinline__ float quantise(const float (&y)[NV], uint32_t (&q)[NV / 4]) {
+  float amax = 0.f, v[NV];
+  bool odd = false;
+  static_for<NV / 2>([&](auto i) {
+    odd |= __builtin_isunordered(y[2 * i], y[2 * i + 1]);
+  });
+  static_for<NV>([&](auto i) {
+    v[i] = y[i];
+    amax = __builtin_fmaxf(amax, __builtin_fabsf(y[i]));   // past a NaN
+  });
+  odd |= amax == __builtin_inff();
+  if (wave_ballot(odd) != 0) {
+    amax = 0.f;
+    static_for<NV>([&](auto i) {
+      // both become e4m3's NaN: an infinity could be cut off at 448
+      const bool fine = __builtin_fabsf(y[i]) < __builtin_inff();
+      v[i] = fine ? y[i] : __builtin_nanf("");
+      amax = __builtin_fmaxf(amax, fine ? __builtin_fabsf(y[i]) : 0.f);
+    });
+  }
+  const BlockScale b = block_scale(group_max<LANES>(amax));
+  static_for<NV / 4>([&](auto i) {
+    int w = __builtin_amdgcn_cvt_pk_fp8_f32(v[4 * i] * b.by, v[4 * i + 1] * b.by, 0, false);
+    w = __builtin_amdgcn_cvt_pk_fp8_f32(v[4 * i + 2] * b.by, v[4 * i + 3] * b.by, w, true);
+    q[i] = (uint32_t)w;
+  });
+  return b.scale;
+}
+
+// A lane's 8-bit values, four or eight of them, past the caches.
+template <int W>
+__device__ __forceinline__ void store_bytes(uint8_t* to, const uint32_t (&q)[W]) {
+  if constexpr (W == 2) {
+    typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+    __builtin_nontemporal_store(u32x2{q[0], q[1]}, reinterpret_cast<u32x2*>(to));
+  } else {
+    static_assert(W == 1, "16-bit or fp32 rows");
+    __builtin_nontemporal_store(q[0], reinterpret_cast<uint32_t*>(to));
+  }
 }
 
 }  // namespace

@@ -42,8 +42,8 @@ struct NormBwdArgs {
   float* partial;           // norm_bwd_partials(T, H, dtype) rows of H
   float eps;
 };
-// Rows of partial weight gradients: one for each row of blocks, a number that
-// the layout alone fixes.
+// Rows of partial weight gradients: one for each block, a number that the layout
+// alone fixes.
 int64_t norm_bwd_partials(const Dims& d);
 hipError_t launch_rms_norm_bwd(const Dims& d, const NormBwdArgs& a, int num_cus,
                                hipStream_t stream);

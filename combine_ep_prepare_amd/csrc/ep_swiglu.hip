@@ -146,25 +146,16 @@ __global__ void __launch_bounds__(kThreads)
           gv = __builtin_nontemporal_load(gate_up + r * 2 * V + v);
           uv = __builtin_nontemporal_load(gate_up + r * 2 * V + V + v);
         }
-        float o[N], amax = 0.f;
+        float o[N];
         static_for<N>([&](auto j) {
           const float g = P::template get<j>(gv);
           const Gate k = gate_of<DT == EP_DTYPE_FP32>(g);
           o[j] = g * k.p * k.r * (P::template get<j>(uv) * k.p);
-          amax = __builtin_fmaxf(amax, finite_magnitude(o[j]));
         });
-        const BlockScale s = block_scale(group_max<kLanes>(amax));
-        scale = s.scale;
-        static_for<N / 4>([&](auto j) {
-          q[j] = to_e4m3(o[4 * j] * s.by, o[4 * j + 1] * s.by, o[4 * j + 2] * s.by,
-                         o[4 * j + 3] * s.by);
-        });
+        scale = quantise<kLanes>(o, q);
       }
       if (source >= 0 || r >= live || d.fill_pads) {
-        if (in) {
-          uint32_t* to = reinterpret_cast<uint32_t*>(out_q + r * d.H) + (int64_t)v * (N / 4);
-          static_for<N / 4>([&](auto j) { to[j] = q[j]; });
-        }
+        if (in) store_bytes(out_q + r * d.H + (int64_t)v * N, q);
         // with the last block, the columns past it too, fewer than eight
         if (lane == 0 || (b == B - 1 && lane < S - b))
           out_scales[r * S + b + lane] = lane == 0 ? scale : 0.f;

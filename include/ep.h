@@ -531,7 +531,7 @@ ep_status_t ep_rms_norm(const ep_layout_t* layout, const void* x, const void* re
                         float* out_scales, hipStream_t stream);
 
 /* Bytes of device memory that ep_rms_norm_bwd needs for its weight gradient, at
- * most 1024 * H * 4; 0 for an invalid layout. Host only. */
+ * most 512 * H * 4; 0 for an invalid layout. Host only. */
 size_t ep_rms_norm_bwd_workspace(const ep_layout_t* layout);
 
 /*

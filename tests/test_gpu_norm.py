@@ -155,7 +155,7 @@ def test_norm_bwd(T, H, dtype):
     # of their magnitudes, and r's 40 u three times over in n c
     bound = 256 * U * mag
     assert ((gx.double() - want).abs() <= rounded(want, bound, dt)).all()
-    # a sum of T terms: a chain of T / partials, then at most 1024 partials
+    # a sum of T terms: a chain of T / partials, then at most 512 partials
     chain = T + 64
     bound_w = (chain + 64) * U * mag_w
     assert ((gw.double() - want_w).abs() <= rounded(want_w, bound_w, dt)).all()
