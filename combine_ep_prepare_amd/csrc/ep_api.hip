@@ -158,7 +158,7 @@ LayerSpace layer_space(const Dims& d, int64_t inner) {
   const size_t routes = (size_t)(d.T * d.K);
   LayerSpace s;
   s.act = align256(sizeof(uint32_t) * (size_t)kLayerCounters);
-  s.y = s.act + align256(routes * (size_t)inner * 2);
+  s.y = s.act + align256(routes * (size_t)inner * 2 * 2);
   s.bytes = s.y + align256(routes * (size_t)d.H * sizeof(float));
   return s;
 }

@@ -19,7 +19,12 @@ namespace epmi {
 namespace {
 
 constexpr int kMaxRoutes = EP_MAX_LAYER_ROUTES;
-constexpr int kRowTile = 16;
+// Rows of x that a matrix instruction takes, and routes of an expert that a tile
+// has: as many in the first product, half in the second, where a route's
+// activations are two rows (see below).
+constexpr int kRows = 16;
+template <bool UP>
+constexpr int kRoutes = UP ? kRows : kRows / 2;
 
 // The routing table in LDS: the expert of each route, kNone without a valid one,
 // and a bit for each expert that has a route.
@@ -74,10 +79,11 @@ struct Active {
 };
 
 // The expert's routes in ascending order: how many, and number first + i of them
-// in each lane i below 16 (and so in i + 16, i + 32, i + 48), as far as there are;
+// in each lane i below ROUTES (and so in i + ROUTES and on), as far as there are;
 // the last one beyond. `mine` is the wavefront's own.
+template <int ROUTES>
 __device__ __forceinline__ int32_t routes_of(const Routes& r, int32_t n, int32_t expert,
-                                             int32_t first, uint16_t (&mine)[kRowTile],
+                                             int32_t first, uint16_t (&mine)[kRows],
                                              int32_t& route) {
   const int lane = lane_id();
   int32_t rows = 0;
@@ -87,12 +93,12 @@ __device__ __forceinline__ int32_t routes_of(const Routes& r, int32_t n, int32_t
     const bool hit = s < n && r.of[s] == expert;
     const uint64_t hits = wave_ballot(hit);
     const int32_t at = rows + __popcll(hits & ((1ull << lane) - 1)) - first;
-    if (hit && at >= 0 && at < kRowTile) mine[at] = (uint16_t)s;
+    if (hit && at >= 0 && at < ROUTES) mine[at] = (uint16_t)s;
     rows += __popcll(hits);
   }
   __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-  const int32_t last = rows - first < kRowTile ? rows - first - 1 : kRowTile - 1;
-  const int32_t i = lane & 15;
+  const int32_t last = rows - first < ROUTES ? rows - first - 1 : ROUTES - 1;
+  const int32_t i = lane % ROUTES;
   route = mine[i < last ? i : last];
   return rows;
 }
@@ -122,7 +128,7 @@ __device__ __forceinline__ f32x4 get_product(const float* from) {
   return v;
 }
 
-// A tile is up to 16 rows of an expert by COLS / 2 columns of gate and the same of
+// A tile is up to kRoutes routes of an expert by COLS / 2 columns of gate and the same of
 // up (UP), or by COLS columns of the second product. The wavefronts take the steps
 // of k in turn and add their sums in LDS at the end, by when each has the first
 // loads of the block's next tile in flight. An expert's row tiles follow each
@@ -133,9 +139,10 @@ __global__ void __launch_bounds__(WAVES* kWave)
   using S = Lines<F, DT, COLS>;
   constexpr int kThreads = WAVES * kWave, kHalf = COLS / 2;
   constexpr int kTileCols = UP ? kHalf : COLS, kQuads = kTileCols / 4;
+  constexpr int kTile = kRoutes<UP>;
   extern __shared__ __align__(16) char mem[];      // WAVES * S::kLds
   __shared__ Routes routes;
-  __shared__ uint16_t row_lists[WAVES][kRowTile];
+  __shared__ uint16_t row_lists[WAVES][kRows];
   __shared__ uint32_t last;
   const int32_t n = (int32_t)(d.T * d.K);
   const int32_t H = (int32_t)d.H, I = (int32_t)a.I;
@@ -184,7 +191,7 @@ __global__ void __launch_bounds__(WAVES* kWave)
   struct Place {
     typename S::Source src;
     int32_t tile, n0;
-    int32_t first, rows;   // first row of the row tile, rows of the expert
+    int32_t first, rows;   // first of the tile's routes, routes of the expert
     int32_t route;         // of the lane's row
   };
   // Starts the loads of a tile: the weights', whose place the expert tells, before
@@ -224,9 +231,12 @@ __global__ void __launch_bounds__(WAVES* kWave)
     }
     const bool mine = wave < K / S::kStep;
     if (mine) s.template load_weights<false>(p.src, wave * S::kStep, K);
-    p.rows = routes_of(routes, n, e, first, row_lists[wave], p.route);
+    p.rows = routes_of<kTile>(routes, n, e, first, row_lists[wave], p.route);
+    // the second product: the high parts of eight routes' activations in the rows,
+    // then the low ones
     p.src.x = UP ? static_cast<const char*>(a.tokens) + (int64_t)(p.route / d.K) * H * 2
-                 : static_cast<const char*>(a.act) + (int64_t)p.route * I * 2;
+                 : static_cast<const char*>(a.act) +
+                       (int64_t)(p.route + (i16 < kTile ? 0 : n)) * I * 2;
     if (mine) s.template load_x<false>(p.src, wave * S::kStep, K);
     return p;
   };
@@ -251,15 +261,15 @@ __global__ void __launch_bounds__(WAVES* kWave)
     // the last tile's products have been acknowledged (all loads are used up: this
     // waits for nothing else)
     if constexpr (!UP) asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
-    const bool done = cur.first + kRowTile >= cur.rows;   // of this tile's expert
-    const int32_t rows = done ? cur.rows - cur.first : kRowTile;
+    const bool done = cur.first + kTile >= cur.rows;   // of this tile's expert
+    const int32_t rows = done ? cur.rows - cur.first : kTile;
     next.tile = done ? cur.tile + (int32_t)gridDim.x : cur.tile;
-    if (next.tile < tiles) next = start(next.tile, done ? 0 : cur.first + kRowTile);
+    if (next.tile < tiles) next = start(next.tile, done ? 0 : cur.first + kTile);
     S::put_sums(lds, acc);
     __syncthreads();
     if constexpr (!UP) raise();
     // four columns of a row at a time
-    for (int i = threadIdx.x; i < kRowTile * kQuads; i += kThreads) {
+    for (int i = threadIdx.x; i < kTile * kQuads; i += kThreads) {
       const int m = i / kQuads, c = i % kQuads * 4;
       const int32_t route = __shfl(cur.route, m, kWave);
       if (m < rows && cur.n0 + c < cols_all) {
@@ -272,11 +282,23 @@ __global__ void __launch_bounds__(WAVES* kWave)
             const Gate g = gate_of<false>(v[k.value]);
             o[k.value] = v[k.value] * g.p * g.r * (u[k.value] * g.p);
           });
-          // the second product's operand: rounded to the payload type, as its
-          // matrix instructions take it
-          *reinterpret_cast<u32x2*>(static_cast<uint16_t*>(a.act) + at) = round_four<DT>(o);
+          // The second product's operand: its matrix instructions take the payload
+          // type, so an activation is kept as the sum of two such values, each a row
+          // of it. Rounded to one, it would add as much to the result's error as that's
+          // own rounding. An expert has few routes: the rows are there anyway.
+          const u32x2 high = round_four<DT>(o);
+          f32x4 rest;
+          static_for<4>([&](auto k) {
+            const uint32_t bits = (high[k.value / 2] >> (k.value % 2 * 16)) & 0xFFFFu;
+            const float h = DT == EP_DTYPE_BF16 ? __uint_as_float(bits << 16) : f16_to_f32(bits);
+            // past the type's range, and NaN: nothing to add
+            rest[k.value] = __builtin_fabsf(h) < __builtin_inff() ? o[k.value] - h : 0.f;
+          });
+          uint16_t* act = static_cast<uint16_t*>(a.act) + at;
+          *reinterpret_cast<u32x2*>(act) = high;
+          *reinterpret_cast<u32x2*>(act + (int64_t)n * I) = round_four<DT>(rest);
         } else {
-          put_product(a.y + at, v);
+          put_product(a.y + at, v + S::template sum_of<WAVES>(mem, kTile + m, c));
         }
       }
     }

@@ -69,7 +69,8 @@ struct LayerArgs {
   const float* down_scales;
   void* result;
   // the workspace's parts: one counter for each column tile of the second
-  // product, activations [T*K, I] of the payload type, products [T*K, H]
+  // product, activations [2, T*K, I] as sums of two values of the payload type,
+  // products [T*K, H]
   uint32_t* counters;
   void* act;
   float* y;

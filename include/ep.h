@@ -589,10 +589,11 @@ ep_status_t ep_grouped_linear_scaled(const ep_layout_t* layout, const void* hand
 /*
  * A whole expert layer for a few tokens, without a prepared handle: for every
  * token, over its valid routes k ascending, with e = topk_idx[t,k],
- *   a         = payload(silu(gate_up[e,:I,:] x) * (gate_up[e,I:,:] x)),  x = tokens[t,:]
+ *   a         = silu(gate_up[e,:I,:] x) * (gate_up[e,I:,:] x),  x = tokens[t,:]
  *   result[t] = payload(sum over k of topk_weights[t,k] * (down[e] a))
  * the products and the weighted sum in fp32 (the first term a product, each later
- * one a fused multiply-add). A route whose id is outside [0,E), masked or not,
+ * one a fused multiply-add); a is held as the sum of two values of the payload
+ * type, to 16 (bf16) or 22 bits (fp16: infinite past its range). A route whose id is outside [0,E), masked or not,
  * counts nothing; a token with no valid route gets +0; an expert may come more
  * than once. T*K is at most EP_MAX_LAYER_ROUTES; uses the layout's num_tokens,
  * topk, num_experts, hidden and dtype (bf16 or fp16; fp32 is EP_ERR_SHAPE). For

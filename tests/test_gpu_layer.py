@@ -3,8 +3,9 @@
 Bounds, step by step: the first product's sums (n steps of 2^-23 of the terms'
 magnitudes for n terms, and 4 steps more a block of scaled weights); the activation,
 whose slope in the gate is below 1.1 of |up| and in up |silu|, 24 + 2 |gate| units of
-2^-24 of its own (the exponent's rounding grows with the gate) and one rounding to the payload type; the second product's sums over terms
-off by that; K weighted terms in fp32; one rounding.
+2^-24 of its own (the exponent's rounding grows with the gate), held as the sum of
+two values of the payload type: half a step of half a step off; the second product's
+sums, of twice as many terms, off by that; K weighted terms in fp32; one rounding.
 """
 import pytest
 import torch
@@ -55,7 +56,7 @@ class Layer:
         tiny = torch.finfo(self.dt).smallest_normal * half
         T = self.x.shape[0]
         want, bound = (torch.zeros(T, H, dtype=torch.float64) for _ in range(2))
-        n1, n2 = H + 4 * (-(-H // 128)), I + 4 * (-(-I // 128))
+        n1, n2 = H + 4 * (-(-H // 128)), 2 * I + 4 * (-(-I // 128))
         for e in range(self.E):
             t, k = (self.idx == e).nonzero(as_tuple=True)
             if not len(t):
@@ -66,7 +67,7 @@ class Layer:
             a = g * torch.sigmoid(g) * u
             silu = (g * torch.sigmoid(g)).abs()
             ea = 1.1 * eg * (u.abs() + eu) + silu * eu + (24 + 2 * g.abs()) * U * a.abs()
-            ea = ea + half * (a.abs() + ea) + tiny
+            ea = ea + half * half * (a.abs() + ea) + tiny
             y, mag = a @ w2.t(), (a.abs() + ea) @ w2.abs().t()
             ey = ea @ w2.abs().t() + n2 * 2.0 ** -23 * mag
             w = self.tw[t, k].double()[:, None]
