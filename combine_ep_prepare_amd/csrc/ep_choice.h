@@ -17,6 +17,10 @@ enum class Kernel {
   kTile128,
   kTile128Once,
   kTile64,
+  // ep_scaled.hip alone: tiles with a ring of buffers
+  kRing64,
+  kRing128,
+  kRing64x128,
 };
 
 // The most rows that all experts together can have: a route has one at most, and
@@ -78,30 +82,44 @@ inline Kernel kernel_of(Product p, const Dims& d, int64_t N, int num_cus) {
 // 128 experts, 2048 inputs and 1536 outputs unless another size is named.
 inline Kernel scaled_kernel_of(const Dims& d, int64_t N, int num_cus) {
   const int64_t rows = most_rows(d) / d.E;
-  // up to 8 rows: 8 rows 67 us against 68 with the tiles below, 4 rows 64 against
-  // 69, one 41 against 46; 12 rows 75 against 71, 16 rows 97 against 73. One expert
-  // has no more rows than there are: 16 of 4096 x 4096 take 10 against 16
-  if (rows <= 8 || (d.E == 1 && rows <= 16)) return Kernel::kFewRows;
-  const int64_t tiles256 = (rows + 255) / 256 * ((N + 255) / 256) * d.E;
-  const int64_t tiles128 = (rows + 127) / 128 * ((N + 127) / 128) * d.E;
+  // up to 6 rows: 6 rows 64 us against 65 with the tiles below, 2 rows 55 against 60;
+  // 8 rows 68 against 62. One expert's few tiles leave most CUs without work, so that
+  // up to 32 rows those of 16 are ahead (4096 x 4096: 32 rows 12 against 17, 64 rows
+  // 18 against 17)
+  if (rows <= 6 || (d.E == 1 && rows <= 32)) return Kernel::kFewRows;
+  // Small grids, by the tiles that an expert of somewhat more rows than the average
+  // (their spread is about its root) needs. Up to a tile of 64 x 64 a CU: those
+  // (one expert of 96 rows, 4096 x 4096: 17 us against 20 with a ring). Up to two and
+  // a little: with a ring of four buffers (8 experts, 4096 x 4096: 16 rows 25 against
+  // 29, 48 rows 26 against 30 with rings of 128). Up to one of 128 x 128 a CU: a ring
+  // of those (64 rows 30 against 36 to 43, 96 rows 31 against 37; 7 experts of 476
+  // rows, 1040 x 776: 13.2 against 13.9; 128 rows, where many have two tiles, 55
+  // against 43 without a ring)
+  int64_t root = 0;
+  while (root * root < rows) ++root;
+  const int64_t more = rows + root, limit = (int64_t)num_cus * 23 / 20;
+  const int64_t tiles64 = (more + 63) / 64 * ((N + 63) / 64) * d.E;
+  if (tiles64 <= num_cus) return Kernel::kTile64;
+  if (tiles64 <= 2 * limit) return Kernel::kRing64;
+  if ((more + 127) / 128 * ((N + 127) / 128) * d.E <= limit) return Kernel::kRing128;
+  // up to 40 rows tiles of 64 x 128, three buffers, weights past the caches: 8 rows 62
+  // us against 68 with tiles of 128, 32 rows 74 against 81, 40 rows 77 against 83, 56
+  // rows 97 against 88 (64 experts, 7168 x 4096: 39 rows 326 against 341, 47 rows 354
+  // against 349)
+  if (rows <= 40) return Kernel::kRing64x128;
   // 256 x 256 tiles from 105 rows: 112 rows 102 us against 113, 96 rows 99 against
   // 92; from 41 where the contraction is deep (64 experts, 7168 x 4096: 63 rows 359
-  // against 363, 95 rows 374 against 388, 31 rows 331 against 330). They have to fill
-  // the CUs, or half of them where their rows would fill two tiles of 128 (8
-  // experts, 4096 x 4096: 256 rows 60 against 78, 128 rows 50 against 43).
-  if ((rows > 104 || (rows > 40 && d.H >= 4096)) &&
-      tiles256 >= (rows > 128 ? num_cus / 2 : num_cus)) {
+  // against 363, 95 rows 374 against 388). They have to fill the CUs, or half of them
+  // where their rows would fill two tiles of 128 (8 experts, 4096 x 4096: 256 rows 60
+  // against 78, 128 rows 50 against 43).
+  const int64_t tiles256 = (rows + 255) / 256 * ((N + 255) / 256) * d.E;
+  if ((rows > 104 || d.H >= 4096) && tiles256 >= (rows > 128 ? num_cus / 2 : num_cus)) {
     // the weights past the caches while most experts have one row tile: 160 rows 112
     // us against 120, 192 rows 117 against 127; 256 rows of 8 experts 62 against 60,
     // 4096 rows of 8 (4096 x 28672) 4700 against 4040
     return rows <= 192 ? Kernel::kTile256Once : Kernel::kTile256;
   }
-  // 64 x 64 tiles where larger ones would leave CUs without work (one expert of 256
-  // rows, 4096 x 4096: 22 us against 31; 7 of 476 rows, 1040 x 776: 13.9 against
-  // 14.3), or would give each one tile of few rows (8 experts: 32 rows 33 against 39,
-  // 64 rows 36 against 40, but 128 rows 62 against 43)
-  if (tiles128 < num_cus || (rows <= 64 && tiles128 < 2 * num_cus)) return Kernel::kTile64;
-  // weights past the caches up to 104 rows: 24 rows 77 us against 84, 96 rows 92
+  // weights past the caches up to 104 rows: 48 rows 87 us against 91, 96 rows 92
   // against 100, but 128 rows 134 against 132
   return rows <= 104 ? Kernel::kTile128Once : Kernel::kTile128;
 }

@@ -417,7 +417,7 @@ __global__ void __launch_bounds__(WM* WN* kWave)
   write_zero_rows(*hv.header, hv, d, out, N * 2 / 16);
 }
 
-template <int DT, int BM, int BN, int WM, int WN, bool ONCE = false>
+template <int DT, int BM, int BN, int WM, int WN, bool ONCE>
 hipError_t launch_scaled_tiles(const Dims& d, const HandleView& hv, const uint8_t* x,
                                const float* x_scales, const uint8_t* w, const float* w_scales,
                                void* out, int64_t N, int num_cus, int per_cu,
@@ -438,14 +438,189 @@ hipError_t launch_scaled_tiles(const Dims& d, const HandleView& hv, const uint8_
   return hipGetLastError();
 }
 
+// Smaller tiles, where a grid leaves a CU few wavefronts and steps are short: a
+// ring of STAGES buffers of a step each, all but one of them asked for ahead, and
+// one sync a step: the step's buffer has landed for all wavefronts, and the one that
+// the step before read is free again. Layout, scales and results as above.
+template <int DT, int BM, int BN, int WM, int WN, int STAGES, bool ONCE>
+__global__ void __launch_bounds__(WM* WN* kWave)
+    scaled_ring_kernel(Dims d, HandleView hv, const uint8_t* __restrict__ x,
+                       const float* __restrict__ x_scales, const uint8_t* __restrict__ w,
+                       const float* __restrict__ w_scales, uint16_t* __restrict__ out,
+                       int64_t N) {
+  using A = Operand<kBytes8, true, BM, WM>;
+  using B = Operand<kBytes8, true, BN, 1>;
+  constexpr int kTileWaves = WM * WN;
+  constexpr int MF = BM / WM / 16, NF = BN / WN / 16;
+  constexpr int kStage = A::kBytes + B::kBytes;
+  constexpr int AL = A::kLoads / kTileWaves, BL = B::kLoads / kTileWaves;
+  static_assert(AL * kTileWaves == A::kLoads && BL * kTileWaves == B::kLoads, "whole loads");
+  static_assert(BN / WN <= kScaleBlock && NF % 2 == 0, "one column scale, results in pairs");
+  static_assert(STAGES <= 4, "two sets of row scales");
+  constexpr int kShare = BM / kTileWaves, kScaleBytes = (BM + 64 - kShare) * 16;
+  extern __shared__ __align__(1024) char lds[];
+  int32_t* tile_start = reinterpret_cast<int32_t*>(lds + STAGES * kStage + 2 * kScaleBytes);
+
+  const int32_t my_rows = rows_of_thread(hv, d);
+  const HandleHeader hh = *hv.header;
+  if (!handle_matches(hh, d)) {
+    if (blockIdx.x == 0 && threadIdx.x == 0) atomicOr(&hv.header->status, EP_STATUS_LAYOUT);
+    return;
+  }
+  const int32_t H = (int32_t)d.H;
+  const int32_t steps = pieces(H, kScaleBlock), SX = (int32_t)EP_SCALE_COLUMNS(H);
+  const int32_t NB = (int32_t)((N + kScaleBlock - 1) / kScaleBlock);
+  const int32_t ct = (int32_t)((N + BN - 1) / BN);
+  const int64_t tiles = (int64_t)list_tiles<kTileWaves * kWave>(hv, d, BM, my_rows, tile_start,
+                                                                tile_start + d.E + 1) * ct;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+  const int wm = wave / WN, wn = wave % WN;
+  const int lane = lane_id();
+  const uint32_t lds_base = (uint32_t)(uintptr_t)(lds_char*)lds;
+  const uint32_t scale_base = lds_base + STAGES * kStage;
+  uint32_t a_at[2], b_at[2];   // of either half of k
+  static_for<2>([&](auto i) {
+    a_at[i.value] = lds_base + A::at(wm * 16, i.value);
+    b_at[i.value] = lds_base + A::kBytes + B::at(wn * (BN / WN), i.value);
+  });
+  const uint32_t s_at = scale_base + (wm * 16 + (lane & 15)) * 16;
+  const int64_t slots = gridDim.x / kRunXcds;
+  const int64_t xcd = blockIdx.x % kRunXcds, slot = blockIdx.x / kRunXcds;
+  for (int64_t t = xcd * slots + slot; t < tiles; t += gridDim.x) {
+    const int e = __builtin_amdgcn_readfirstlane(
+        expert_of_tile(tile_start, d.E, (int32_t)(t / ct)));
+    const int32_t rts = tile_start[e + 1] - tile_start[e];
+    const int64_t in_e = t - (int64_t)tile_start[e] * ct;
+    const int32_t group = (int32_t)(in_e / ((int64_t)kGroup * ct));
+    const int32_t in_g = (int32_t)(in_e - (int64_t)group * kGroup * ct);
+    const int32_t gm = rts - group * kGroup < kGroup ? rts - group * kGroup : kGroup;
+    const int32_t mi = __builtin_amdgcn_readfirstlane(group * kGroup + in_g % gm);
+    const int64_t n0 = __builtin_amdgcn_readfirstlane((in_g / gm) * BN);
+    const Segment s = segment_of(hv, d, e);
+    const int32_t height = (int32_t)((((int64_t)s.rows + rts - 1) / rts + 15) / 16 * 16);
+    const int64_t m0 = (int64_t)mi * height;
+    const int32_t mrows = (int32_t)(s.rows - m0 < height ? s.rows - m0 : height);
+    const int32_t ncols = (int32_t)(N - n0 < BN ? N - n0 : BN);
+    const char* a_src = reinterpret_cast<const char*>(x) + (s.row + m0) * H;
+    const char* b_src = reinterpret_cast<const char*>(w) + ((int64_t)e * N + n0) * H;
+    const float* s_src = x_scales + (s.row + m0) * SX;
+    uint32_t a_off[AL], b_off[BL];
+    static_for<AL>([&](auto i) { a_off[i] = A::source(wave * AL + i, (uint32_t)H, 0); });
+    static_for<BL>([&](auto i) { b_off[i] = B::source(wave * BL + i, (uint32_t)H, 0); });
+    const uint32_t s_off = (uint32_t)(wave * kShare + lane) * (uint32_t)(SX * 4);
+
+    // Step k into its buffer, and with every fourth the row scales of four; a step
+    // past the last has empty buffers, whose loads put zeros into LDS.
+    auto load = [&](int k) {
+      const uint32_t k0 = (uint32_t)k * A::kDepth;
+      const int32_t left = rest_after(H, k0);
+      const uint32_t gone = A::chunk_k() < left ? 0 : kOutside;
+      const uint32_t to = lds_base + k % STAGES * kStage;
+      if (k % 4 == 0)
+        load_to_lds<false, 0>(
+            buffer_of(s_src, left > 0 ? (uint32_t)mrows * (uint32_t)(SX * 4) : 0),
+            s_off + (uint32_t)k * 4,
+            __builtin_amdgcn_readfirstlane(scale_base + k / 4 % 2 * kScaleBytes +
+                                           wave * kShare * 16));
+      const row16_t ab = buffer_of(a_src + k0, left > 0 ? (uint32_t)mrows * (uint32_t)H - k0 : 0);
+      const row16_t bb = buffer_of(b_src + k0, left > 0 ? (uint32_t)ncols * (uint32_t)H - k0 : 0);
+      const uint32_t a_to = __builtin_amdgcn_readfirstlane(to + wave * AL * 1024);
+      const uint32_t b_to = __builtin_amdgcn_readfirstlane(to + A::kBytes + wave * BL * 1024);
+      static_for<AL>([&](auto i) {
+        load_to_lds<false, i.value * 1024>(ab, a_off[i] | gone, a_to);
+      });
+      static_for<BL>([&](auto i) {
+        load_to_lds<ONCE, i.value * 1024>(bb, b_off[i] | gone, b_to);
+      });
+    };
+    const int64_t nb = (n0 + wn * (BN / WN)) / kScaleBlock;
+    const float* w_scale = w_scales + ((int64_t)e * NB + (nb < NB ? nb : NB - 1)) * steps;
+
+    f32x4 acc[MF][NF];
+    static_for<MF>([&](auto i) {
+      static_for<NF>([&](auto j) { acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f}; });
+    });
+    const bool busy = wm * 16 < mrows && wn * (BN / WN) < ncols;
+    static_for<STAGES - 1>([&](auto k) { load(k); });
+    float w_by = w_scale[0];
+    for (int k = 0; k < steps; ++k) {
+      const float w_next = w_scale[k + 1 < steps ? k + 1 : k];
+      // the loads of STAGES - 2 steps may be on their way (where one of them has
+      // scales too, an older one is waited for that need not be)
+      sync_loads<(STAGES - 2) * (AL + BL)>();
+      load(k + STAGES - 1);
+      if (busy) {
+        const uint32_t at = k % STAGES * kStage;
+        row16_t nf[NF][2];
+        static_for<NF>([&](auto j) {
+          static_for<2>([&](auto h) {
+            nf[j][h.value] = B::template read<j.value, h.value>(b_at[h.value] + at);
+          });
+        });
+        static_for<MF>([&](auto i) {
+          row16_t mf[2];
+          static_for<2>([&](auto h) {
+            mf[h.value] = A::template read<i.value, h.value>(a_at[h.value] + at);
+          });
+          const float by =
+              w_by * *reinterpret_cast<const __attribute__((address_space(3))) float*>(
+                         (const lds_char*)(uintptr_t)(s_at + k / 4 % 2 * kScaleBytes + k % 4 * 4 +
+                                                      i.value * WM * 256));
+          static_for<NF>([&](auto j) {
+            const f32x4 sum = mma8(nf[j][0], nf[j][1], mf[0], mf[1]);
+            static_for<4>([&](auto c) {
+              acc[i][j][c.value] = __builtin_fmaf(by, sum[c.value], acc[i][j][c.value]);
+            });
+          });
+        });
+      }
+      w_by = w_next;
+    }
+    sync_loads<0>();  // no load is left in flight, and LDS is free again
+    // a lane holds four consecutive columns of one row of each 16 x 16 block
+    if (busy) {
+      static_for<MF>([&](auto i) {
+        const int32_t m = (i * WM + wm) * 16 + (lane & 15);
+        uint16_t* to = out + (s.row + m0 + m) * N + n0;
+        static_for<NF / 2>([&](auto j) {
+          const row16_t v = join_blocks(round4<DT>(acc[i][2 * j]), round4<DT>(acc[i][2 * j + 1]));
+          const int32_t n = wn * (BN / WN) + j * 32 + (lane >> 4) * 8;
+          if (m < mrows && n < ncols) *reinterpret_cast<row16_t*>(to + n) = v;
+        });
+      });
+    }
+  }
+  write_zero_rows(hh, hv, d, out, N * 2 / 16);
+}
+
+template <int DT, int BM, int BN, int WM, int WN, int STAGES, bool ONCE>
+hipError_t launch_scaled_ring(const Dims& d, const HandleView& hv, const uint8_t* x,
+                              const float* x_scales, const uint8_t* w, const float* w_scales,
+                              void* out, int64_t N, int num_cus, int per_cu, hipStream_t stream) {
+  constexpr int kTileWaves = WM * WN;
+  const int64_t ct = (N + BN - 1) / BN, routes = most_rows(d);
+  int64_t blocks = (routes / BM + (d.E < routes ? d.E : routes)) * ct;
+  const int64_t most = (int64_t)num_cus * per_cu;
+  if (blocks > most) blocks = most;
+  blocks = (blocks + kRunXcds - 1) / kRunXcds * kRunXcds;
+  if (blocks < kRunXcds) blocks = kRunXcds;
+  const size_t lds = STAGES * (size_t)(BM + BN) * 128 +
+                     2 * (size_t)(BM + 64 - BM / kTileWaves) * 16 +
+                     sizeof(int32_t) * (size_t)(d.E + 1 + 16);
+  scaled_ring_kernel<DT, BM, BN, WM, WN, STAGES, ONCE>
+      <<<dim3((uint32_t)blocks), dim3(kTileWaves * kWave), lds, stream>>>(
+          d, hv, x, x_scales, w, w_scales, static_cast<uint16_t*>(out), N);
+  return hipGetLastError();
+}
+
 template <int DT>
 hipError_t launch_few_rows(const Dims& d, const HandleView& hv, const uint8_t* x,
                            const float* x_scales, const uint8_t* w, const float* w_scales,
-                           void* out, int64_t N, int num_cus, hipStream_t stream) {
+                           void* out, int64_t N, int num_cus, int per_cu, hipStream_t stream) {
   const int64_t ct = (N + kCols - 1) / kCols;
   const int64_t routes = most_rows(d);
   int64_t blocks = (routes / kRowTile + (d.E < routes ? d.E : routes)) * ct;
-  const int64_t most = (int64_t)num_cus * kBlocksPerCU;
+  const int64_t most = (int64_t)num_cus * per_cu;
   if (blocks > most) blocks = most;
   if (blocks < 1) blocks = 1;
   const size_t lds = kWaves * (size_t)Lines<kScaled, DT, kCols>::kLds +
@@ -459,28 +634,21 @@ template <int DT>
 hipError_t launch_product(const Dims& d, const HandleView& hv, const uint8_t* x,
                           const float* x_scales, const uint8_t* w, const float* w_scales,
                           void* out, int64_t N, int num_cus, hipStream_t stream) {
-  auto tiles = [&](auto size, auto wn, auto once, int per_cu) {
-    constexpr int S = decltype(size)::value;
-    return launch_scaled_tiles<DT, S, S, 2, decltype(wn)::value, decltype(once)::value>(
-        d, hv, x, x_scales, w, w_scales, out, N, num_cus, per_cu, stream);
+  auto go = [&](auto launch, int per_cu) {
+    return launch(d, hv, x, x_scales, w, w_scales, out, N, num_cus, per_cu, stream);
   };
-  using std::integral_constant;
-  constexpr integral_constant<int, 2> two{};
-  constexpr integral_constant<int, 4> four{};
   switch (scaled_kernel_of(d, N, num_cus)) {
-    case Kernel::kFewRows:
-      return launch_few_rows<DT>(d, hv, x, x_scales, w, w_scales, out, N, num_cus, stream);
-    case Kernel::kTile256:
-      return tiles(integral_constant<int, 256>{}, four, std::false_type{}, 1);
-    case Kernel::kTile256Once:
-      return tiles(integral_constant<int, 256>{}, four, std::true_type{}, 1);
-    case Kernel::kTile128:
-      return tiles(integral_constant<int, 128>{}, two, std::false_type{}, 2);
-    case Kernel::kTile128Once:
-      return tiles(integral_constant<int, 128>{}, two, std::true_type{}, 2);
-    case Kernel::kTile64: break;
+    case Kernel::kTile256: return go(launch_scaled_tiles<DT, 256, 256, 2, 4, false>, 1);
+    case Kernel::kTile256Once: return go(launch_scaled_tiles<DT, 256, 256, 2, 4, true>, 1);
+    case Kernel::kTile128: return go(launch_scaled_tiles<DT, 128, 128, 2, 2, false>, 2);
+    case Kernel::kTile128Once: return go(launch_scaled_tiles<DT, 128, 128, 2, 2, true>, 2);
+    case Kernel::kTile64: return go(launch_scaled_tiles<DT, 64, 64, 2, 2, false>, 4);
+    case Kernel::kRing64: return go(launch_scaled_ring<DT, 64, 64, 2, 2, 4, false>, 2);
+    case Kernel::kRing128: return go(launch_scaled_ring<DT, 128, 128, 2, 4, 4, false>, 1);
+    case Kernel::kRing64x128: return go(launch_scaled_ring<DT, 64, 128, 2, 4, 3, true>, 2);
+    case Kernel::kFewRows: break;
   }
-  return tiles(integral_constant<int, 64>{}, two, std::false_type{}, 4);
+  return go(launch_few_rows<DT>, kBlocksPerCU);
 }
 
 }  // namespace

@@ -32,18 +32,22 @@ def kernel(tmp_path_factory):
     return choose
 
 
+RING64, RING128, RING64x128 = range(6, 9)
+
+
 def test_rules_at_their_borders(kernel):
     def rows(r, H=2048, N=1536, E=128):
         return kernel(r * E // 8, 8, E, H, N)
-    assert [rows(r) for r in (0, 1, 8, 9, 104, 105, 192, 193)] == \
-        [FEW, FEW, FEW, T128_ONCE, T128_ONCE, T256_ONCE, T256_ONCE, T256]
-    assert [rows(r, 7168, 4096, 64) for r in (8, 40, 41, 193)] == \
-        [FEW, T128_ONCE, T256_ONCE, T256]
-    # eight experts of 4096 x 4096: one tile of 128 a CU, or one of 256 for two CUs
-    assert [rows(r, 4096, 4096, 8) for r in (9, 64, 65, 128, 129)] == \
-        [T64, T64, T128_ONCE, T128, T256_ONCE]
+    assert [rows(r) for r in (0, 1, 6, 7, 40, 41, 104, 105, 192, 193)] == \
+        [FEW, FEW, FEW, RING64x128, RING64x128, T128_ONCE, T128_ONCE, T256_ONCE, T256_ONCE, T256]
+    assert [rows(r, 7168, 4096, 64) for r in (6, 40, 41, 193)] == \
+        [FEW, RING64x128, T256_ONCE, T256]
+    # eight experts of 4096 x 4096: two tiles of 64 a CU, one of 128, one of 256 for two
+    assert [rows(r, 4096, 4096, 8) for r in (7, 56, 57, 117, 118, 128, 129)] == \
+        [RING64, RING64, RING128, RING128, T128, T128, T256_ONCE]
     # one expert
-    assert [kernel(r, 1, 1, 4096, 4096) for r in (16, 17, 256)] == [FEW, T64, T64]
+    assert [kernel(r, 1, 1, 4096, 4096) for r in (32, 33, 240, 241, 512)] == \
+        [FEW, T64, T64, RING64, RING64]
     # a share of the experts: the capacity tells
     assert kernel(64, 8, 32, 7168, 4096, cap=80) == FEW
     assert kernel(32768, 8, 32, 7168, 4096, cap=41000) == T256
@@ -51,8 +55,8 @@ def test_rules_at_their_borders(kernel):
 
 def test_loads_into_lds(tmp_path):
     text = "\n".join(_device_asm(os.path.join(_build.CSRC, "ep_scaled.hip"), str(tmp_path)))
-    kernels = _kernels(text, "scaled_product_kernel")
-    assert len(kernels) == 10
+    kernels = _kernels(text, "scaled_product_kernel") + _kernels(text, "scaled_ring_kernel")
+    assert len(kernels) == 16
     for name, body in kernels:
         check_m0(name, body)
         ins = list(_instructions(body.splitlines()))
@@ -81,6 +85,7 @@ def test_scalar_registers_and_scratch(tmp_path, source):
         assert int(scratch) <= (20 if large else 0), f"{name}: {scratch} bytes of scratch a lane"
     # and none of them inside the steps, where a wait for it would be one for every load
     for name, body in _kernels(text, "scaled_product_kernel"):
+        assert "v_mfma" in body
         for block in re.split(r"^\.LBB\S+:.*$", body, flags=re.M):
             if block.count("v_mfma") >= 4:
                 assert "scratch_" not in block, name
