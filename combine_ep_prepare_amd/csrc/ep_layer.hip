@@ -149,8 +149,8 @@ __global__ void __launch_bounds__(WAVES* kWave)
   const int32_t K = UP ? H : I;                    // of this product
   const int32_t cols_all = UP ? I : H;             // columns of either half, or all
   if constexpr (UP) {
-    // the second product's counters
-    for (int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x; i < kLayerCounters;
+    // the second product's counters, one for each of its column tiles at most
+    for (int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x; i < pieces(H, 32);
          i += (int64_t)gridDim.x * kThreads)
       a.counters[i] = 0;
   }

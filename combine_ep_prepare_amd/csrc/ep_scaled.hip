@@ -110,8 +110,11 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerCU)
 }
 
 // Row tiles of an expert whose column tiles run together: with the columns
-// dealt after them, the tiles in flight on an XCD share both operands.
-constexpr int kGroup = 6;
+// dealt after them, the tiles in flight on an XCD share both operands. 8 experts of
+// 4096 rows, 4096 x 28672: 3530 us, against 3577 with 8, 3636 with 6 and 3645 with 12
+// (14336 x 4096: 1670, 1671, 1736, 1751; a share of 32 experts, 7168 x 4096: 928, 924,
+// 916, 915).
+constexpr int kGroup = 4;
 
 // Many rows: the tiled product of ep_linear.hip with steps of 128 values of k, one
 // block of scales each. WM x WN wavefronts hold every WM-th block of 16 rows and

@@ -22,14 +22,17 @@ from typing import List, Optional, Sequence, Tuple
 import torch
 from torch import Tensor
 
-from . import (DTYPE_BF16, LAYOUT_NO_PAD_FILL, LAYOUT_ZERO_TAIL, TORCH_DTYPE, Layout,
+from . import (DTYPE_BF16, E4M3, LAYOUT_NO_PAD_FILL, LAYOUT_ZERO_TAIL, TORCH_DTYPE, Layout,
                combine as _combine,
                combine_bwd as _combine_bwd, combine_weighted as _combine_weighted,
                combine_weighted_bwd as _combine_weighted_bwd, dispatch as _dispatch,
-               dispatch_bwd as _dispatch_bwd, grouped_linear as _grouped_linear,
-               grouped_linear_bwd as _grouped_linear_bwd,
-               grouped_linear_quant as _grouped_linear_quant, prepare as _prepare,
-               swiglu as _swiglu, swiglu_bwd as _swiglu_bwd)
+               dispatch_bwd as _dispatch_bwd, expert_layer as _expert_layer,
+               grouped_linear as _grouped_linear, grouped_linear_bwd as _grouped_linear_bwd,
+               grouped_linear_quant as _grouped_linear_quant,
+               grouped_linear_scaled as _grouped_linear_scaled, new_expert_layer_workspace,
+               new_rms_norm_bwd_workspace, prepare as _prepare, rms_norm as _rms_norm,
+               rms_norm_bwd as _rms_norm_bwd, scale_columns, swiglu as _swiglu,
+               swiglu_bwd as _swiglu_bwd, swiglu_scaled as _swiglu_scaled)
 
 NS = "ep_mi355x"
 
@@ -376,3 +379,193 @@ def _swiglu_backward(ctx, g):
 
 
 swiglu.register_autograd(_swiglu_backward, setup_context=_swiglu_setup)
+
+
+# --------------------------------------------------------------------------
+# the norm in front of a layer, the ops in 8 bits, the layer for a few tokens
+# --------------------------------------------------------------------------
+
+def _norm_layout(x: Tensor) -> Layout:
+    return Layout(x.shape[0], 1, 1, 1, x.shape[1], 0, dtype=x.dtype)
+
+
+@torch.library.custom_op(f"{NS}::rms_norm", mutates_args=())
+def rms_norm(x: Tensor, weight: Tensor, eps: float) -> Tensor:
+    """The norm of the rows of x [T,H] times weight [H]."""
+    out = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+    _rms_norm(_norm_layout(x), x, weight, eps, out=out)
+    return out
+
+
+@rms_norm.register_fake
+def _(x, weight, eps):
+    return x.new_empty(x.shape)
+
+
+@torch.library.custom_op(f"{NS}::add_rms_norm", mutates_args=())
+def add_rms_norm(x: Tensor, residual: Tensor, weight: Tensor,
+                 eps: float) -> Tuple[Tensor, Tensor]:
+    """(the norm of x + residual times weight, x + residual)."""
+    out, total = (torch.empty(x.shape, dtype=x.dtype, device=x.device) for _ in range(2))
+    _rms_norm(_norm_layout(x), x, weight, eps, out=out, residual=residual, sum_out=total)
+    return out, total
+
+
+@add_rms_norm.register_fake
+def _(x, residual, weight, eps):
+    return x.new_empty(x.shape), x.new_empty(x.shape)
+
+
+@torch.library.custom_op(f"{NS}::rms_norm_bwd", mutates_args=())
+def rms_norm_bwd(grad: Tensor, x: Tensor, weight: Tensor, eps: float,
+                 grad_sum: Optional[Tensor]) -> Tuple[Tensor, Tensor]:
+    """The gradients of what the norm was of and of the weight."""
+    L = _norm_layout(x)
+    gx = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+    gw = torch.empty(weight.shape, dtype=weight.dtype, device=weight.device)
+    _rms_norm_bwd(L, grad, x, weight, eps, gx, gw, new_rms_norm_bwd_workspace(L, x.device),
+                  grad_sum)
+    return gx, gw
+
+
+@rms_norm_bwd.register_fake
+def _(grad, x, weight, eps, grad_sum):
+    return x.new_empty(x.shape), weight.new_empty(weight.shape)
+
+
+# The first alone, for a backward that is not asked for the weight's.
+
+@torch.library.custom_op(f"{NS}::rms_norm_grad_x", mutates_args=())
+def rms_norm_grad_x(grad: Tensor, x: Tensor, weight: Tensor, eps: float,
+                    grad_sum: Optional[Tensor]) -> Tensor:
+    """The gradient of what the norm was of alone."""
+    gx = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+    _rms_norm_bwd(_norm_layout(x), grad, x, weight, eps, gx, grad_sum=grad_sum)
+    return gx
+
+
+@rms_norm_grad_x.register_fake
+def _(grad, x, weight, eps, grad_sum):
+    return x.new_empty(x.shape)
+
+
+def _norm_gradients(ctx, want_w, g, g_sum):
+    x, weight = ctx.saved_tensors
+    if want_w:
+        return rms_norm_bwd(g.contiguous(), x, weight, ctx.eps, g_sum)
+    return rms_norm_grad_x(g.contiguous(), x, weight, ctx.eps, g_sum), None
+
+
+def _norm_setup(ctx, inputs, output):
+    x, weight, ctx.eps = inputs
+    ctx.save_for_backward(x, weight)
+
+
+def _norm_backward(ctx, g):
+    gx, gw = _norm_gradients(ctx, ctx.needs_input_grad[1], g, None)
+    return gx, gw, None
+
+
+rms_norm.register_autograd(_norm_backward, setup_context=_norm_setup)
+
+
+def _add_norm_setup(ctx, inputs, output):
+    ctx.eps = inputs[3]
+    ctx.save_for_backward(output[1], inputs[2])
+
+
+def _add_norm_backward(ctx, g, g_sum):
+    gx, gw = _norm_gradients(ctx, ctx.needs_input_grad[2], g, g_sum.contiguous())
+    return gx, gx, gw, None
+
+
+add_rms_norm.register_autograd(_add_norm_backward, setup_context=_add_norm_setup)
+
+
+@torch.library.custom_op(f"{NS}::rms_norm_scaled", mutates_args=())
+def rms_norm_scaled(x: Tensor, weight: Tensor, eps: float) -> Tuple[Tensor, Tensor]:
+    """``rms_norm`` in 8 bits: (e4m3 [T,H], scales [T, scale_columns(H)]); no autograd,
+    like the ops below."""
+    q = torch.empty(x.shape, dtype=E4M3, device=x.device)
+    scales = torch.empty(x.shape[0], scale_columns(x.shape[1]), dtype=torch.float32,
+                         device=x.device)
+    _rms_norm(_norm_layout(x), x, weight, eps, out_q=q, out_scales=scales)
+    return q, scales
+
+
+@rms_norm_scaled.register_fake
+def _(x, weight, eps):
+    return (x.new_empty(x.shape, dtype=E4M3),
+            x.new_empty((x.shape[0], scale_columns(x.shape[1])), dtype=torch.float32))
+
+
+@torch.library.custom_op(f"{NS}::add_rms_norm_scaled", mutates_args=())
+def add_rms_norm_scaled(x: Tensor, residual: Tensor, weight: Tensor,
+                        eps: float) -> Tuple[Tensor, Tensor, Tensor]:
+    """(e4m3, scales, x + residual)."""
+    q = torch.empty(x.shape, dtype=E4M3, device=x.device)
+    scales = torch.empty(x.shape[0], scale_columns(x.shape[1]), dtype=torch.float32,
+                         device=x.device)
+    total = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+    _rms_norm(_norm_layout(x), x, weight, eps, out_q=q, out_scales=scales, residual=residual,
+              sum_out=total)
+    return q, scales, total
+
+
+@add_rms_norm_scaled.register_fake
+def _(x, residual, weight, eps):
+    return (x.new_empty(x.shape, dtype=E4M3),
+            x.new_empty((x.shape[0], scale_columns(x.shape[1])), dtype=torch.float32),
+            x.new_empty(x.shape))
+
+
+@torch.library.custom_op(f"{NS}::swiglu_scaled", mutates_args=())
+def swiglu_scaled(gate_up: Tensor, handle: Tensor, layout: List[int]) -> Tuple[Tensor, Tensor]:
+    """``swiglu`` in 8 bits: (e4m3 [cap,I], scales [cap, scale_columns(I)])."""
+    hidden = gate_up.shape[1] // 2
+    q = torch.empty(gate_up.shape[0], hidden, dtype=E4M3, device=gate_up.device)
+    scales = torch.empty(gate_up.shape[0], scale_columns(hidden), dtype=torch.float32,
+                         device=gate_up.device)
+    _swiglu_scaled(_rows_layout(layout, hidden), handle, gate_up, q, scales)
+    return q, scales
+
+
+@swiglu_scaled.register_fake
+def _(gate_up, handle, layout):
+    cap, hidden = gate_up.shape[0], gate_up.shape[1] // 2
+    return (gate_up.new_empty((cap, hidden), dtype=E4M3),
+            gate_up.new_empty((cap, scale_columns(hidden)), dtype=torch.float32))
+
+
+@torch.library.custom_op(f"{NS}::grouped_linear_scaled", mutates_args=())
+def grouped_linear_scaled(x: Tensor, x_scales: Tensor, weight: Tensor, weight_scales: Tensor,
+                          handle: Tensor, layout: List[int]) -> Tensor:
+    """``grouped_linear`` of 8-bit operands, a result of the layout's payload type."""
+    out = torch.empty(x.shape[0], weight.shape[1], dtype=_pdtype(layout), device=x.device)
+    _grouped_linear_scaled(_rows_layout(layout, x.shape[1]), handle, x, x_scales, weight,
+                           weight_scales, out)
+    return out
+
+
+@grouped_linear_scaled.register_fake
+def _(x, x_scales, weight, weight_scales, handle, layout):
+    return x.new_empty((x.shape[0], weight.shape[1]), dtype=_pdtype(layout))
+
+
+@torch.library.custom_op(f"{NS}::expert_layer", mutates_args=())
+def expert_layer(tokens: Tensor, topk_idx: Tensor, topk_weights: Tensor, gate_up: Tensor,
+                 down: Tensor, gate_up_scales: Optional[Tensor],
+                 down_scales: Optional[Tensor]) -> Tensor:
+    """A whole expert layer for a few tokens [T,H]."""
+    out = torch.empty(tokens.shape, dtype=tokens.dtype, device=tokens.device)
+    L = Layout(tokens.shape[0], topk_idx.shape[1], down.shape[0], 1, tokens.shape[1], 0,
+               dtype=tokens.dtype)
+    _expert_layer(L, topk_idx, topk_weights, tokens, gate_up, down, out,
+                  new_expert_layer_workspace(L, down.shape[2], tokens.device), gate_up_scales,
+                  down_scales)
+    return out
+
+
+@expert_layer.register_fake
+def _(tokens, topk_idx, topk_weights, gate_up, down, gate_up_scales, down_scales):
+    return tokens.new_empty(tokens.shape)

@@ -270,7 +270,9 @@ def test_gradients_are_refused():
 
 @pytest.mark.parametrize("kind,T,K,E,A,H,N", [
     ("any", 140, 2, 40, 1, 528, 520), ("steep", 900, 2, 16, 4, 272, 1160),   # 64 x 64 tiles
-    ("any", 1200, 2, 64, 1, 272, 1032), ("masked", 1500, 4, 64, 8, 656, 1048),   # 128 x 128
+    ("any", 1200, 2, 64, 1, 272, 1032), ("steep", 1200, 2, 64, 1, 272, 1032),   # 64 x 128
+    ("masked", 1500, 4, 64, 8, 656, 1048), ("any", 960, 1, 8, 1, 400, 4104),   # 128 x 128
+    ("steep", 1000, 1, 8, 2, 272, 4104),
     ("any", 6000, 2, 96, 1, 272, 1032), ("steep", 9000, 2, 64, 4, 400, 1288),   # 256 x 256
     ("any", 3300, 2, 8, 16, 144, 4104), ("one", 700, 1, 2, 1, 272, 16392),
     ("any", 1700, 2, 64, 1, 4112, 1032)])
@@ -278,3 +280,9 @@ def test_linear_tiles(kind, T, K, E, A, H, N):
     """Every tile size, of whole numbers: ragged rows, features, segments and last
     blocks, tiles with part of their rows, experts without any."""
     linear_case(Case(kind, T, K, E, A, "bf16", seed=T), H, N, whole=True)
+
+
+@pytest.mark.parametrize("T,H,N", [(16400, 144, 136), (216000, 16, 264)])
+def test_linear_many_experts(T, H, N):
+    """The most experts, with a few rows each and with many: the longest tile lists."""
+    linear_case(Case("any", T, 1, 2048, 1, "bf16", seed=1), H, N, whole=True)
