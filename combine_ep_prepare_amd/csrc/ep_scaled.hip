@@ -9,12 +9,24 @@
 // the outer one fp32 multiply-adds.
 
 #include "ep_choice.h"
+#include "ep_gate.h"
 #include "ep_lines.h"
 #include "ep_tiles.h"
 
 namespace epmi {
 
 namespace {
+
+// A lane's sums in two neighbouring blocks of 16 columns, four each, rounded and
+// traded for eight side by side (join_blocks). Rounded in whole numbers, as a NaN
+// wants it, the large tile's sums took 4096 cycles of the 100000 of a tile of 32
+// steps; see pack().
+template <int DT>
+__device__ __forceinline__ row16_t round_and_join(f32x4 a, f32x4 b) {
+  const float o[8] = {a[0], a[1], a[2], a[3], b[0], b[1], b[2], b[3]};
+  const row16_t r = pack<DT>(o);
+  return join_blocks(u32x2{r[0], r[1]}, u32x2{r[2], r[3]});
+}
 
 constexpr int kWaves = 4;             // wavefronts of a block: they split k
 constexpr int kThreads = kWaves * kWave;
@@ -408,7 +420,7 @@ __global__ void __launch_bounds__(WM* WN* kWave)
         const int32_t m = (i * WM + wm) * 16 + (place & 15);
         uint16_t* to = out + (s.row + m0 + m) * N + n0;
         static_for<NF / 2>([&](auto j) {
-          const row16_t v = join_blocks(round4<DT>(acc[i][2 * j]), round4<DT>(acc[i][2 * j + 1]));
+          const row16_t v = round_and_join<DT>(acc[i][2 * j], acc[i][2 * j + 1]);
           const int32_t n = wn * (BN / WN) + j * 32 + (place >> 4) * 8;
           if (m < mrows && n < ncols) *reinterpret_cast<row16_t*>(to + n) = v;
         });
@@ -586,7 +598,7 @@ __global__ void __launch_bounds__(WM* WN* kWave)
         const int32_t m = (i * WM + wm) * 16 + (lane & 15);
         uint16_t* to = out + (s.row + m0 + m) * N + n0;
         static_for<NF / 2>([&](auto j) {
-          const row16_t v = join_blocks(round4<DT>(acc[i][2 * j]), round4<DT>(acc[i][2 * j + 1]));
+          const row16_t v = round_and_join<DT>(acc[i][2 * j], acc[i][2 * j + 1]);
           const int32_t n = wn * (BN / WN) + j * 32 + (lane >> 4) * 8;
           if (m < mrows && n < ncols) *reinterpret_cast<row16_t*>(to + n) = v;
         });
