@@ -34,8 +34,9 @@ constexpr int kCols = 64;             // columns of a tile: within a scale's 128
 constexpr int kRowTile = 16;          // rows of a tile
 constexpr int kBlocksPerCU = 4;
 
-// Up to 16 rows of an expert by kCols columns a block step (see ep_lines.h). The
-// wavefronts take the steps of k in turn, so that the block reads 512 bytes of a
+// Up to 16 rows of an expert by kCols columns a block step (see ep_lines.h); bound by
+// the weights' bytes, which it reads at 6.9 TB/s (32 tokens by top-8 of 256, 7168 x
+// 4096: 694 us). The wavefronts take the steps of k in turn, so that the block reads 512 bytes of a
 // column side by side, and add their sums in LDS at the end; by then each has the
 // first loads of the block's next tile in flight.
 template <int DT>
@@ -139,6 +140,15 @@ constexpr int kGroup = 4;
 // instructions run. A row's scales come through LDS too, four steps' at a time, 16
 // bytes a row; the columns' one of a step is the same for a wavefront, whose columns
 // lie in one block.
+//
+// 8 experts of 4096 rows: 2200 TFLOP/s at 4096 x 28672, 2340 at 14336 x 4096 (a
+// library product of 8-bit operands without scales 3000). The clock falls to 1.6 GHz
+// on random operands (2650 TFLOP/s on zeros), and the matrix units are busy 53% of
+// its cycles: two wavefronts a SIMD leave them idle around the syncs, and the
+// multiply-adds take a tenth (2350 TFLOP/s without). More than 256 registers a
+// wavefront would let a larger part read less from LDS, but only instructions of the
+// matrix unit reach the second half of the file, and the sums need others. 32 x 32 x
+// 64 instructions, whose 16 sums a lane spill, ran at 1970.
 template <int DT, int BM, int BN, int WM, int WN, bool ONCE>
 __global__ void __launch_bounds__(WM* WN* kWave)
     scaled_product_kernel(Dims d, HandleView hv, const uint8_t* __restrict__ x,
