@@ -36,9 +36,9 @@ constexpr int kBlocksPerCU = 4;
 
 // Up to 16 rows of an expert by kCols columns a block step (see ep_lines.h); bound by
 // the weights' bytes, which it reads at 6.9 TB/s (32 tokens by top-8 of 256, 7168 x
-// 4096: 694 us). The wavefronts take the steps of k in turn, so that the block reads 512 bytes of a
-// column side by side, and add their sums in LDS at the end; by then each has the
-// first loads of the block's next tile in flight.
+// 4096: 694 us). The wavefronts take the steps of k in turn, so that the block reads
+// 512 bytes of a column side by side, and add their sums in LDS at the end; by then
+// each has the first loads of the block's next tile in flight.
 template <int DT>
 __global__ void __launch_bounds__(kThreads, kBlocksPerCU)
     few_rows_scaled_kernel(Dims d, HandleView hv, const uint8_t* __restrict__ x,
@@ -179,8 +179,9 @@ __global__ void __launch_bounds__(WM* WN* kWave)
   const int32_t steps = pieces(all_H, kScaleBlock), SX = (int32_t)EP_SCALE_COLUMNS(all_H);
   const int32_t NB = (int32_t)((N + kScaleBlock - 1) / kScaleBlock);
   const int32_t all_ct = (int32_t)((N + BN - 1) / BN);
-  const int64_t tiles = (int64_t)list_tiles<kTileWaves * kWave>(hv, d, BM, my_rows, tile_start,
-                                                                tile_start + d.E + 1) * all_ct;
+  // a scalar: as a pair of vector registers it would be spilled over the steps
+  const int64_t tiles = (int64_t)__builtin_amdgcn_readfirstlane(list_tiles<kTileWaves * kWave>(
+                            hv, d, BM, my_rows, tile_start, tile_start + d.E + 1)) * all_ct;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
   const int wm = wave / WN, wn = wave % WN;
   const int lane = lane_id();
