@@ -490,7 +490,7 @@ def rms_norm(layout: Layout, x: torch.Tensor, weight: torch.Tensor, eps: float,
              sum_out: Optional[torch.Tensor] = None, stream=None):
     """The norm of x [T,H] (with a residual: of sum_out = x + residual) times
     weight [H], into out [T,H], or in 8 bits into out_q with out_scales
-    [T, scale_columns(H)], or both."""
+    [T, scale_columns(H)], or both. sum_out may be residual (or x) itself."""
     T, H, dtype = layout.num_tokens, layout.hidden, layout.payload_dtype
     if out is None and out_q is None:
         raise ValueError("out or out_q is required")

@@ -353,7 +353,7 @@ def dispatch_scaled(q: torch.Tensor, scales: torch.Tensor, topk_weights: torch.T
     (recv_q, recv_scales, recv_topk_weights), bit copies."""
     _rows(q, "q")
     _rows(scales, "scales")
-    _serving_only("dispatch_scaled", topk_weights)
+    _serving_only("dispatch_scaled", q, scales, topk_weights)
     if q.dtype != E4M3 or scales.shape[1] != scale_columns(q.shape[1]):
         raise ValueError(f"{tuple(q.shape)} {q.dtype} and scales {tuple(scales.shape)} are not "
                          "rows in 8 bits with their scales")
@@ -374,7 +374,7 @@ def grouped_linear_scaled(x: torch.Tensor, x_scales: torch.Tensor, weight: torch
     """``grouped_linear`` of 8-bit operands (the binding's layout of their scales)
     with a result of ``dtype`` (bf16 or fp16): [cap,N]."""
     _rows(x, "x")
-    _serving_only("grouped_linear_scaled", x_scales, weight_scales)
+    _serving_only("grouped_linear_scaled", x, x_scales, weight, weight_scales)
     if weight.dim() != 3:
         raise ValueError(f"weight must have shape (E, N, H), got {tuple(weight.shape)}")
     L = routing.layout_for(dtype, x.shape[1])

@@ -49,7 +49,8 @@
  *  - Work is enqueued on `stream` and nothing waits for it: no call below
  *    synchronises, allocates, frees or keeps a pointer after it returns,
  *    except ep_read_status, which waits for the stream. The caller owns
- *    every buffer. Outputs must not overlap inputs or each other.
+ *    every buffer. Outputs must not overlap inputs or each other, but where
+ *    a call says that they may.
  *  - Host-detectable errors return an ep_status_t before any HIP call is
  *    made; nothing is enqueued then. Data-dependent errors raise sticky bits
  *    in the handle's status word (see ep_read_status).
@@ -514,12 +515,13 @@ ep_status_t ep_swiglu_bwd(const ep_layout_t* layout, const void* handle_mem,
  *   y = s / sqrt(mean(s^2) + eps) * weight
  * in fp32, given as out (rounded once), as out_q with out_scales, or as both.
  * The norm is that of the rounded sum, which the gradient is taken at. hidden up
- * to EP_MAX_NORM_FEATURES; with out_q a multiple of 16; eps 0 or more. Uses the layout's
- * num_tokens, hidden and dtype.
+ * to EP_MAX_NORM_FEATURES; with out_q a multiple of 16; eps 0 or more (with 0 a
+ * row of zeros gives NaN). Uses the layout's num_tokens, hidden and dtype.
  *   x           payload [T,H]
  *   residual    payload [T,H] or NULL
  *   weight      payload [H]
- *   sum         payload [T,H]; NULL iff residual is
+ *   sum         payload [T,H]; NULL iff residual is; may be residual or x
+ *               itself, which is then updated in place
  *   out         payload [T,H] or NULL
  *   out_q       e4m3 [T,H] or NULL; out and out_q are not both NULL
  *   out_scales  fp32 [T, EP_SCALE_COLUMNS(H)]; NULL iff out_q is

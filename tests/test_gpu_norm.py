@@ -99,6 +99,23 @@ def test_norm(T, H, dtype, residual):
     assert torch.equal(q.view(torch.uint8), q2.view(torch.uint8)) and torch.equal(sc, sc2)
 
 
+@pytest.mark.parametrize("T,H", [(5, 520), (1030, 264), (4, 4096), (2, 7168), (2, 16384)])
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+def test_sum_in_place(T, H, dtype):
+    """The residual's buffer, or x's, takes the sum: the same bits as another one."""
+    dt = DT[dtype]
+    x, w, gen = values(T, H, dt, H + 5)
+    res = torch.randn(T, H, generator=gen).to(dt).cuda()
+    L = ep.Layout(T, 1, 1, 1, H, 0, dtype=dt)
+    out, s, out2 = torch.empty_like(x), torch.empty_like(x), torch.empty_like(x)
+    ep.rms_norm(L, x, w, EPS, out=out, residual=res, sum_out=s)
+    for a, b, into in ((x, res.clone(), 1), (x.clone(), res, 0)):
+        out2.fill_(7.0)
+        total = (a, b)[into]
+        ep.rms_norm(L, a, w, EPS, out=out2, residual=b, sum_out=total)
+        assert torch.equal(out, out2) and torch.equal(s, total)
+
+
 @pytest.mark.parametrize("dtype", ["bf16", "fp32"])
 def test_special_rows(dtype):
     """Rows of zeros, tiny and huge rows, an infinity, a NaN: each its own row's

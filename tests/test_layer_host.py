@@ -174,3 +174,13 @@ def test_binding_checks():
         ep.new_rms_norm_bwd_workspace(lay(H=16400))
     with pytest.raises(ValueError, match="invalid layout or inner"):
         ep.new_expert_layer_workspace(L, 12)
+
+
+def test_eight_bit_weights_that_want_a_gradient():
+    from combine_ep_prepare_amd import autograd as epa
+    q, w = torch.zeros(4, 64, dtype=ep.E4M3), torch.zeros(1, 64, 64, dtype=ep.E4M3)
+    s = torch.zeros(4, ep.scale_columns(64))
+    with pytest.raises(RuntimeError, match="no backward"):
+        epa.grouped_linear_scaled(q, s, w.requires_grad_(), s, None)
+    with pytest.raises(RuntimeError, match="no backward"):
+        epa.dispatch_scaled(q, s.clone().requires_grad_(), torch.zeros(4, 1), None)
