@@ -25,7 +25,8 @@ struct Gate {
 // leave out into p and refines the reciprocal by a step: s is then within 20
 // units of 2^-24 of its value at any g, in the time that the rows' bytes take
 // anyway (8192 rows by top-2, 4096 values out: 146 us with it and without).
-template <bool EXACT>
+// SHORT, for the kernel that the arithmetic bounds, rounds 1 + e once.
+template <bool EXACT, bool SHORT = false>
 __device__ __forceinline__ Gate gate_of(float g) {
   constexpr double kLog2e = 1.44269504088896340736;
   constexpr float kHi = (float)kLog2e, kLo = (float)(kLog2e - (double)kHi);
@@ -42,7 +43,7 @@ __device__ __forceinline__ Gate gate_of(float g) {
   } else {
     root = __builtin_amdgcn_exp2f(__builtin_fabsf(g) * (-0.5f * kHi));
   }
-  const float e = root * root, d = 1.f + e;
+  const float e = root * root, d = SHORT ? __builtin_fmaf(root, root, 1.f) : 1.f + e;
   o.r = __builtin_amdgcn_rcpf(d);
   if constexpr (EXACT) o.r = __builtin_fmaf(__builtin_fmaf(-d, o.r, 1.f), o.r, o.r);
   o.p = g < 0.f ? root : 1.f;

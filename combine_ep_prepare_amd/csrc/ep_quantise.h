@@ -9,45 +9,63 @@ namespace epmi {
 
 namespace {
 
-// The largest of m over aligned groups of LANES lanes (a power of two up to 32),
-// in every lane of the group.
+// The largest of m, 0 or more, over aligned groups of LANES lanes (16 or 32), in
+// every lane of the group. Numbers of that sign are in the order of their bits; a
+// lane's neighbours come within the instruction that compares them.
 template <int LANES>
 __device__ __forceinline__ float group_max(float m) {
-  static_for<5>([&](auto i) {
-    if constexpr ((1 << i) < LANES) m = __builtin_fmaxf(m, __shfl_xor(m, 1 << i, kWave));
-  });
-  return m;
+  static_assert(LANES == 16 || LANES == 32, "16-bit or fp32 rows");
+  uint32_t v = __float_as_uint(m);
+  auto with = [&](auto order) {
+    const uint32_t o = (uint32_t)__builtin_amdgcn_mov_dpp((int)v, order.value, 0xf, 0xf, true);
+    v = o > v ? o : v;
+  };
+  using std::integral_constant;
+  with(integral_constant<int, 0xB1>{});    // lanes 1, 0, 3, 2 of four
+  with(integral_constant<int, 0x4E>{});    // 2, 3, 0, 1
+  with(integral_constant<int, 0x141>{});   // eight backwards
+  with(integral_constant<int, 0x140>{});   // sixteen backwards
+  if constexpr (LANES == 32) {
+    const uint32_t o = (uint32_t)__shfl_xor((int)v, 16, kWave);
+    v = o > v ? o : v;
+  }
+  return __uint_as_float(v);
 }
 
-// A block's scale, and what its values are multiplied by: the reciprocal of the
-// scale but for its rounding, so that q is off the definition's quotient only
-// where that lies next to the middle of two e4m3 values.
+// A block's scale, and its reciprocal, which the values are multiplied by: q is off
+// the definition's quotient only where that lies next to the middle of two e4m3
+// values. Each is a product or a reciprocal with the rest that it leaves put back,
+// good to its last bit; between 2^-100 and 2^120 nothing overflows or is subnormal.
 struct BlockScale {
   float scale, by;
 };
 __device__ __forceinline__ BlockScale block_scale(float amax) {
+  constexpr float kInverse = 1.f / kE4m3Max;
   const float m = __builtin_fmaxf(amax, kLeastAmax);
-  return BlockScale{m / kE4m3Max, kE4m3Max / m};
+  const float q = m * kInverse;
+  const float scale = __builtin_fmaf(__builtin_fmaf(-kE4m3Max, q, m), kInverse, q);
+  const float r = __builtin_amdgcn_rcpf(scale);
+  return BlockScale{scale, __builtin_fmaf(__builtin_fmaf(-scale, r, 1.f), r, r)};
 }
 
 // NV values of a block, of which a group of LANES lanes holds NV each, to e4m3, four
 // to a word; returns the scale. Called by whole groups. Values that are not finite
-// are looked for once, by the wavefront, and taken apart only where there are any:
-// apart from that a value costs its maximum, half a comparison, a product and half a
-// conversion.
+// are looked for by the wavefront, in scalars, and taken apart only where there are
+// any: apart from that a value costs its maximum, half a comparison, a product and
+// half a conversion.
 template <int LANES, int NV>
 __device__ __forceinline__ float quantise(const float (&y)[NV], uint32_t (&q)[NV / 4]) {
   float amax = 0.f, v[NV];
-  bool odd = false;
+  uint64_t odd = 0;
   static_for<NV / 2>([&](auto i) {
-    odd |= __builtin_isunordered(y[2 * i], y[2 * i + 1]);
+    odd |= wave_ballot(__builtin_isunordered(y[2 * i], y[2 * i + 1]));
   });
   static_for<NV>([&](auto i) {
     v[i] = y[i];
     amax = __builtin_fmaxf(amax, __builtin_fabsf(y[i]));   // past a NaN
   });
-  odd |= amax == __builtin_inff();
-  if (wave_ballot(odd) != 0) {
+  odd |= wave_ballot(amax == __builtin_inff());
+  if (odd != 0) {
     amax = 0.f;
     static_for<NV>([&](auto i) {
       // both become e4m3's NaN: an infinity could be cut off at 448

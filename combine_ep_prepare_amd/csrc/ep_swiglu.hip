@@ -101,7 +101,10 @@ __global__ void __launch_bounds__(kThreads)
 // The activation with its result in 8 bits. The values of a scale lie side by
 // side in a row: 16 (fp32: 32) neighbouring lanes hold them, 16 bytes of each
 // half a lane, and the scale's maximum takes four (five) exchanges. Rows are
-// dealt by such blocks in address order.
+// dealt by such blocks in address order. 32768 rows of 14336 values 412 us, 5.8
+// TB/s; uneven experts' 65536 rows of 768 52. Both were bound by the arithmetic (421
+// and 61 us) while a value took 32 vector instructions, for rows of a step in 64
+// bits, a shuffle an exchange, IEEE quotients and a flag a value: it takes 19.
 template <int DT>
 __global__ void __launch_bounds__(kThreads)
     swiglu_scaled_kernel(Dims d, HandleView hv, const row16_t* __restrict__ gate_up,
@@ -124,18 +127,27 @@ __global__ void __launch_bounds__(kThreads)
   const int32_t row_by = kGroups / B, b_by = kGroups % B;
   for (int64_t r0 = (int64_t)blockIdx.x * step_rows; r0 < rows;
        r0 += (int64_t)gridDim.x * step_rows) {
-    const int64_t r1 = r0 + step_rows < rows ? r0 + step_rows : rows;
-    int64_t r = r0 + row_first;
-    int32_t b = b_first;
-    int32_t source = r < r1 && r < live ? hv.row_src[r] : -1;
-    while (r < r1) {
-      int64_t next_r = r + row_by;
-      int32_t next_b = b + b_by;
+    // from here on rows and places count from r0 on: 32 bits hold a step's bytes
+    auto of_step = [&](int64_t n) {
+      return (int32_t)(n - r0 < 0 ? 0 : n - r0 < step_rows ? n - r0 : step_rows);
+    };
+    const int32_t here = of_step(rows), alive = of_step(live);
+    const char* gate = reinterpret_cast<const char*>(gate_up + r0 * 2 * V);
+    const char* up = gate + (int64_t)V * 16;
+    uint8_t* to_q = out_q + r0 * d.H;
+    char* to_scales = reinterpret_cast<char*>(out_scales + r0 * S);
+    const char* sources = reinterpret_cast<const char*>(hv.row_src + r0);
+    auto source_of = [&](int32_t r) {
+      return r < alive ? *reinterpret_cast<const int32_t*>(sources + (uint32_t)r * 4) : -1;
+    };
+    int32_t r = row_first, b = b_first, source = source_of(r);
+    while (r < here) {
+      int32_t next_r = r + row_by, next_b = b + b_by;
       if (next_b >= B) {
         next_b -= B;
         ++next_r;
       }
-      const int32_t next_source = next_r < r1 && next_r < live ? hv.row_src[next_r] : -1;
+      const int32_t next_source = source_of(next_r);
       const int32_t v = b * kLanes + lane;
       const bool in = v < V;
       uint32_t q[N / 4] = {};
@@ -143,22 +155,24 @@ __global__ void __launch_bounds__(kThreads)
       if (source >= 0) {
         row16_t gv = {0, 0, 0, 0}, uv = {0, 0, 0, 0};
         if (in) {
-          gv = __builtin_nontemporal_load(gate_up + r * 2 * V + v);
-          uv = __builtin_nontemporal_load(gate_up + r * 2 * V + V + v);
+          const uint32_t at = (uint32_t)(r * 2 * V + v) * 16;
+          gv = __builtin_nontemporal_load(reinterpret_cast<const row16_t*>(gate + at));
+          uv = __builtin_nontemporal_load(reinterpret_cast<const row16_t*>(up + at));
         }
         float o[N];
         static_for<N>([&](auto j) {
           const float g = P::template get<j>(gv);
-          const Gate k = gate_of<DT == EP_DTYPE_FP32>(g);
+          const Gate k = gate_of<DT == EP_DTYPE_FP32, true>(g);
           o[j] = g * k.p * k.r * (P::template get<j>(uv) * k.p);
         });
         scale = quantise<kLanes>(o, q);
       }
-      if (source >= 0 || r >= live || d.fill_pads) {
-        if (in) store_bytes(out_q + r * d.H + (int64_t)v * N, q);
+      if (source >= 0 || r >= alive || d.fill_pads) {
+        if (in) store_bytes(to_q + (uint32_t)(r * V + v) * N, q);
         // with the last block, the columns past it too, fewer than eight
         if (lane == 0 || (b == B - 1 && lane < S - b))
-          out_scales[r * S + b + lane] = lane == 0 ? scale : 0.f;
+          *reinterpret_cast<float*>(to_scales + (uint32_t)(r * S + b + lane) * 4) =
+              lane == 0 ? scale : 0.f;
       }
       r = next_r;
       b = next_b;
@@ -173,9 +187,8 @@ hipError_t launch_swiglu_scaled(const Dims& d, const HandleView& hv, const void*
                                 uint8_t* out_q, float* out_scales, int num_cus,
                                 hipStream_t stream) {
   // Short blocks, of 512 vectors or a row, each of one step: 32768 rows of 14336 values
-  // 420 us, against 450 with blocks four times as long, 64 a CU, and 432 to 482 with
-  // blocks of 1024 to 256 vectors; uneven experts' rows of 768 62 either way. The
-  // limit keeps the grid's threads below 2^32.
+  // 412 us, 437 with two rows; uneven experts' rows of 768 52, and 59, 53 and 55 with
+  // 256, 1024 and 2048 vectors. The limit keeps the grid's threads below 2^32.
   const int32_t step_rows = (int32_t)((512 + d.V - 1) / d.V);
   int64_t blocks = (d.cap + step_rows - 1) / step_rows;
   const int64_t most = (int64_t)num_cus * 4096;
