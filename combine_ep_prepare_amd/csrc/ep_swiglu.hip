@@ -104,7 +104,7 @@ __global__ void __launch_bounds__(kThreads)
 // dealt by such blocks in address order. 32768 rows of 14336 values 412 us, 5.8
 // TB/s; uneven experts' 65536 rows of 768 52. Both were bound by the arithmetic (421
 // and 61 us) while a value took 32 vector instructions, for rows of a step in 64
-// bits, a shuffle an exchange, IEEE quotients and a flag a value: it takes 19.
+// bits, a shuffle an exchange, IEEE quotients and a flag a value: it takes 22.
 template <int DT>
 __global__ void __launch_bounds__(kThreads)
     swiglu_scaled_kernel(Dims d, HandleView hv, const row16_t* __restrict__ gate_up,
