@@ -152,13 +152,17 @@ bool bytes_ok(int64_t n) { return features_ok(n) && n % 16 == 0; }
 
 // The parts of the workspace of the layer for a few tokens.
 struct LayerSpace {
-  size_t act, y, bytes;
+  size_t act, exps, y, bytes;
 };
 LayerSpace layer_space(const Dims& d, int64_t inner) {
   const size_t routes = (size_t)(d.T * d.K);
   LayerSpace s;
   s.act = align256(sizeof(uint32_t) * (size_t)kLayerCounters);
-  s.y = s.act + align256(routes * (size_t)inner * 2 * 2);
+  s.exps = s.act + align256(routes * (size_t)inner * 2 * 2);
+  // of fp16 activations alone: a byte for every 16 of whole blocks of 128
+  s.y = s.exps + (d.dtype == EP_DTYPE_FP16
+                      ? align256(routes * (size_t)((inner + 127) / 128 * 8))
+                      : 0);
   s.bytes = s.y + align256(routes * (size_t)d.H * sizeof(float));
   return s;
 }
@@ -629,6 +633,7 @@ ep_status_t ep_expert_layer(const ep_layout_t* layout, const int64_t* topk_idx,
                     result,
                     reinterpret_cast<uint32_t*>(ws),
                     ws + s.act,
+                    reinterpret_cast<uint8_t*>(ws + s.exps),
                     reinterpret_cast<float*>(ws + s.y),
                     inner};
   return launch_expert_layer(d, a, num_cus, stream) == hipSuccess ? EP_OK : EP_ERR_HIP;

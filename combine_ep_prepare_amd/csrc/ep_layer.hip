@@ -138,7 +138,8 @@ __device__ __forceinline__ f32x4 get_product(const float* from) {
 template <int F, int DT, int COLS, int WAVES, bool UP>
 __global__ void __launch_bounds__(WAVES* kWave)
     layer_kernel(Dims d, LayerArgs a) {
-  using S = Lines<F, DT, COLS>;
+  constexpr bool kExps = DT == EP_DTYPE_FP16;      // of the activations
+  using S = Lines<F, DT, COLS, !UP && kExps>;
   constexpr int kThreads = WAVES * kWave, kHalf = COLS / 2;
   constexpr int kTileCols = UP ? kHalf : COLS, kQuads = kTileCols / 4;
   constexpr int kTile = kRoutes<UP>;
@@ -150,6 +151,7 @@ __global__ void __launch_bounds__(WAVES* kWave)
   const int32_t H = (int32_t)d.H, I = (int32_t)a.I;
   const int32_t K = UP ? H : I;                    // of this product
   const int32_t cols_all = UP ? I : H;             // columns of either half, or all
+  const int64_t exps_row = pieces(I, kScaleBlock) * (kScaleBlock / kExpGroup);
   if constexpr (UP) {
     // the second product's counters, one for each of its column tiles at most
     for (int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x; i < pieces(H, 32);
@@ -239,6 +241,7 @@ __global__ void __launch_bounds__(WAVES* kWave)
     p.src.x = UP ? static_cast<const char*>(a.tokens) + (int64_t)(p.route / d.K) * H * 2
                  : static_cast<const char*>(a.act) +
                        (int64_t)(p.route + (i16 < kTile ? 0 : n)) * I * 2;
+    if constexpr (!UP && kExps) p.src.x_exps = a.act_exps + p.route * exps_row;
     if (mine) s.template load_x<false>(p.src, wave * S::kStep, K);
     return p;
   };
@@ -274,20 +277,39 @@ __global__ void __launch_bounds__(WAVES* kWave)
     for (int i = threadIdx.x; i < kTile * kQuads; i += kThreads) {
       const int m = i / kQuads, c = i % kQuads * 4;
       const int32_t route = __shfl(cur.route, m, kWave);
-      if (m < rows && cur.n0 + c < cols_all) {
-        const int64_t at = (int64_t)route * cols_all + cur.n0 + c;
-        const f32x4 v = S::template sum_of<WAVES>(mem, m, c);
-        if constexpr (UP) {
+      const bool there = m < rows && cur.n0 + c < cols_all;
+      const int64_t at = (int64_t)route * cols_all + cur.n0 + c;
+      if constexpr (UP) {
+        f32x4 o = {0.f, 0.f, 0.f, 0.f};
+        if (there) {
+          const f32x4 v = S::template sum_of<WAVES>(mem, m, c);
           const f32x4 u = S::template sum_of<WAVES>(mem, m, kHalf + c);
-          f32x4 o;
           static_for<4>([&](auto k) {
             const Gate g = gate_of<false>(v[k.value]);
             o[k.value] = v[k.value] * g.p * g.r * (u[k.value] * g.p);
           });
-          // The second product's operand: its matrix instructions take the payload
-          // type, so an activation is kept as the sum of two such values, each a row
-          // of it. Rounded to one, it would add as much to the result's error as that's
-          // own rounding. An expert has few routes: the rows are there anyway.
+        }
+        // The second product's operand: its matrix instructions take the payload
+        // type, so an activation is kept as the sum of two such values, each a row
+        // of it. Rounded to one, it would add as much to the result's error as that's
+        // own rounding. An expert has few routes: the rows are there anyway. Two bf16
+        // values hold 16 bits of any fp32 number; two of fp16 hold 22 bits in a part
+        // of its range, to which each 16 of a route are brought by a power of two.
+        if constexpr (kExps) {
+          static_assert(!UP || kTileCols == kExpGroup, "a tile's columns share an exponent");
+          float amax = 0.f;    // past a NaN; an infinity stays one
+          static_for<4>([&](auto k) {
+            amax = __builtin_fmaxf(amax, __builtin_fabsf(o[k.value]));
+          });
+          static_for<2>([&](auto i) {
+            amax = __builtin_fmaxf(amax, __shfl_xor(amax, 1 << i, kWave));
+          });
+          const uint32_t e = exponent_for(amax);
+          o *= inverse_power_of(e);
+          if (there && c == 0)
+            a.act_exps[route * exps_row + cur.n0 / kExpGroup] = (uint8_t)e;
+        }
+        if (there) {
           const u32x2 high = round_four<DT>(o);
           f32x4 rest;
           static_for<4>([&](auto k) {
@@ -299,9 +321,10 @@ __global__ void __launch_bounds__(WAVES* kWave)
           uint16_t* act = static_cast<uint16_t*>(a.act) + at;
           *reinterpret_cast<u32x2*>(act) = high;
           *reinterpret_cast<u32x2*>(act + (int64_t)n * I) = round_four<DT>(rest);
-        } else {
-          put_product(a.y + at, v + S::template sum_of<WAVES>(mem, kTile + m, c));
         }
+      } else if (there) {
+        put_product(a.y + at, S::template sum_of<WAVES>(mem, m, c) +
+                                  S::template sum_of<WAVES>(mem, kTile + m, c));
       }
     }
     __syncthreads();

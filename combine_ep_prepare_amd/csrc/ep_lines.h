@@ -83,8 +83,38 @@ enum Form {
               // sum is that of the e4m3 values themselves, and scaled in fp32
 };
 
+// Rows of x in fp16 with exponents: kExpGroup neighbours are kept as values of up to
+// 2^15, the largest of them 2^14 at least, times a power of two of theirs, so that
+// what fp32 holds is neither past fp16's range nor among its subnormals. The power is
+// given by its exponent bits as an fp32 number, a byte. A byte of 1 or more and of 240
+// or less: the power and its inverse are normal numbers.
+constexpr int kExpGroup = 16;
+__device__ __forceinline__ uint32_t exponent_for(float amax) {
+  const uint32_t e = __float_as_uint(__builtin_fminf(amax, 0x1.fffffep127f)) >> 23;
+  return (e > 15 ? e : 15) - 14;
+}
+__device__ __forceinline__ float power_of(uint32_t exponent) {
+  return __uint_as_float(exponent << 23);
+}
+__device__ __forceinline__ float inverse_power_of(uint32_t exponent) {
+  return __uint_as_float((254 - exponent) << 23);
+}
+
+// Eight fp16 values times 2^by, by <= 0, in two steps of half of it: each factor is
+// an fp16 number down to 2^-44, where nothing is left of a value.
+__device__ __forceinline__ row16_t lower8(row16_t v, int by) {
+  by = by > -44 ? by : -44;
+  const _Float16 f0 = (_Float16)__uint_as_float((uint32_t)(127 + by / 2) << 23);
+  const _Float16 f1 = (_Float16)__uint_as_float((uint32_t)(127 + by - by / 2) << 23);
+  f16x8 h = __builtin_bit_cast(f16x8, v);
+  h = h * f0 * f1;
+  return __builtin_bit_cast(row16_t, h);
+}
+
 // A tile has COLS columns in two halves, which may lie apart (gate and up rows).
-template <int F, int DT, int COLS>
+// EXPS: rows of x with exponents. A step's are brought to the largest one of its row,
+// whose power the step's sums take.
+template <int F, int DT, int COLS, bool EXPS = false>
 struct Lines {
   static constexpr int kSize = F == kPayload ? 2 : 1;       // bytes of a weight
   static constexpr int kStep = 128 / kSize;                 // values of k
@@ -93,15 +123,18 @@ struct Lines {
   static constexpr int kX = F == kWeights8 ? 4 : 2;         // 16-byte parts of x
   static constexpr int kXSize = F == kScaled ? 1 : 2;
   static constexpr int kScales = F == kPayload ? 0 : F == kScaled ? 1 : kNF;
+  static constexpr int kExpWords = EXPS ? kStep / kExpGroup / 4 : 0;   // of a step and row
   static constexpr int kLds = COLS * 128;
   static constexpr int kSumRow = COLS + 4;                  // floats of a row of sums
   static_assert(16 * kSumRow * 4 <= kLds, "the sums fit the weights' place");
+  static_assert(!EXPS || (DT == EP_DTYPE_FP16 && F != kScaled), "rows of fp16 values");
 
   struct Source {
     const char* w[2];            // first column of either half, the same in all lanes
     int32_t cols[2];             // columns of either half that there are, multiples of 8
     const char* x;               // the lane's row of x
     const float* x_scales;       // its scales (kScaled)
+    const uint8_t* x_exps;       // its exponents (EXPS), those of whole steps
     const float* w_scales[kScales > 0 ? kScales : 1];   // of the lane's columns
   };
 
@@ -109,6 +142,7 @@ struct Lines {
   row16_t x[kX];
   float scale[kScales > 0 ? kScales : 1];
   float x_scale;
+  uint32_t exps[kExpWords > 0 ? kExpWords : 1];
 
   // The k, in the step, of part p of this lane's x: the same as that of the
   // weights that multiply() reads beside it.
@@ -149,6 +183,30 @@ struct Lines {
       static_for<kScales>([&](auto i) { scale[i] = s.w_scales[i][block]; });
       if constexpr (F == kScaled) x_scale = s.x_scales[block];
     }
+    static_for<kExpWords>([&](auto i) {
+      const int32_t group = k0 / kExpGroup + i * 4;
+      exps[i] = *reinterpret_cast<const uint32_t*>(s.x_exps + group);
+      if constexpr (PART) {
+        // past the row's groups nothing was written
+        const int32_t have = pieces(K, kExpGroup) - group;
+        exps[i] &= have >= 4 ? 0xFFFFFFFFu : have <= 0 ? 0u : (1u << (have * 8)) - 1;
+      }
+    });
+  }
+  // The step's x to the largest of its exponents, which it returns.
+  __device__ __forceinline__ uint32_t level(row16_t (&xs)[kX], const uint32_t (&ex)[kExpWords > 0 ? kExpWords : 1]) const {
+    uint32_t most = 0;
+    static_for<kExpWords * 4>([&](auto i) {
+      const uint32_t e = (ex[i / 4] >> (i % 4 * 8)) & 0xFF;
+      most = e > most ? e : most;
+    });
+    static_for<kX>([&](auto p) {
+      const int group = input(p) / kExpGroup;
+      const uint32_t word = kExpWords > 1 && p >= kX / 2 ? ex[kExpWords - 1] : ex[0];
+      const uint32_t own = (word >> (group % 4 * 8)) & 0xFF;
+      xs[p] = lower8(xs[p], (int)own - (int)most);
+    });
+    return most;
   }
   template <bool PART>
   __device__ __forceinline__ void load(const Source& s, int32_t k0, int32_t K) {
@@ -176,30 +234,38 @@ struct Lines {
     static_for<kX>([&](auto p) { xs[p] = x[p]; });
     float sc[kScales > 0 ? kScales : 1];
     static_for<kScales>([&](auto i) { sc[i] = F == kScaled ? scale[i] * x_scale : scale[i]; });
+    float power = 1.f;
+    uint32_t ex[kExpWords > 0 ? kExpWords : 1];
+    static_for<kExpWords>([&](auto i) { ex[i] = exps[i]; });
     if constexpr (MORE) load<false>(s, k1, K);
+    if constexpr (EXPS) power = power_of(level(xs, ex));
     const int lane = lane_id(), q = lane >> 4, i16 = lane & 15;
     const char* mine = lds + i16 * 128;
     const int slot0 = (q ^ (i16 & 7)) << 4, slot1 = ((4 + q) ^ (i16 & 7)) << 4;
     static_for<kNF>([&](auto j) {
       const row16_t a = *reinterpret_cast<const row16_t*>(mine + j * 2048 + slot0);
       const row16_t b = *reinterpret_cast<const row16_t*>(mine + j * 2048 + slot1);
-      if constexpr (F == kPayload) {
+      if constexpr (F == kPayload && !EXPS) {
         acc[j] = mma16<DT>(a, xs[0], acc[j]);
         acc[j] = mma16<DT>(b, xs[1], acc[j]);
       } else {
-        f32x4 part;
+        f32x4 part = {0.f, 0.f, 0.f, 0.f};
         if constexpr (F == kScaled) {
           part = mma8(a, b, xs[0], xs[1]);
+        } else if constexpr (F == kPayload) {
+          part = mma16<DT>(a, xs[0], part);
+          part = mma16<DT>(b, xs[1], part);
         } else {
-          part = f32x4{0.f, 0.f, 0.f, 0.f};
           part = mma16<DT>(widen8<DT>(a[0], a[1]), xs[0], part);
           part = mma16<DT>(widen8<DT>(a[2], a[3]), xs[1], part);
           part = mma16<DT>(widen8<DT>(b[0], b[1]), xs[2], part);
           part = mma16<DT>(widen8<DT>(b[2], b[3]), xs[3], part);
         }
+        // the sums of a lane are those of its own row of x
+        float by = power;
+        if constexpr (F != kPayload) by = EXPS ? sc[j] * power : sc[F == kScaled ? 0 : j.value];
         static_for<4>([&](auto c) {
-          acc[j][c.value] =
-              __builtin_fmaf(sc[F == kScaled ? 0 : j.value], part[c.value], acc[j][c.value]);
+          acc[j][c.value] = __builtin_fmaf(by, part[c.value], acc[j][c.value]);
         });
       }
     });

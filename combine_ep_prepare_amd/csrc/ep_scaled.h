@@ -69,10 +69,12 @@ struct LayerArgs {
   const float* down_scales;
   void* result;
   // the workspace's parts: one counter for each column tile of the second
-  // product, activations [2, T*K, I] as sums of two values of the payload type,
+  // product, activations [2, T*K, I] as sums of two values of the payload type, in
+  // fp16 times a power of two for every 16 (exponent bytes [T*K, ceil(I/128) * 8]),
   // products [T*K, H]
   uint32_t* counters;
   void* act;
+  uint8_t* act_exps;
   float* y;
   int64_t I;
 };

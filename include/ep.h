@@ -595,8 +595,10 @@ ep_status_t ep_grouped_linear_scaled(const ep_layout_t* layout, const void* hand
  *   result[t] = payload(sum over k of topk_weights[t,k] * (down[e] a))
  * the products and the weighted sum in fp32 (the first term a product, each later
  * one a fused multiply-add); a is held as the sum of two values of the payload
- * type, to 16 (bf16) or 22 bits (fp16: infinite past its range), and an infinite
- * weight of down may reach its outputs as NaN. A route whose id is outside [0,E),
+ * type, to 16 bits in bf16, and in fp16 with an exponent for every 16 values, to 22
+ * bits or 2^-36 of the largest among the 64 (8-bit weights: 128) that enter the
+ * products together: neither range nor subnormals of the type take anything from
+ * it. An infinite weight of down may reach its outputs as NaN. A route whose id is outside [0,E),
  * masked or not, counts nothing; a token with no valid route gets +0; an expert
  * may come more than once. T*K is at most EP_MAX_LAYER_ROUTES; uses the layout's num_tokens,
  * topk, num_experts, hidden and dtype (bf16 or fp16; fp32 is EP_ERR_SHAPE). For
