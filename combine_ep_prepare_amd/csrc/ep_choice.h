@@ -88,20 +88,25 @@ inline Kernel scaled_kernel_of(const Dims& d, int64_t N, int num_cus) {
   // 18 against 17)
   if (rows <= 6 || (d.E == 1 && rows <= 32)) return Kernel::kFewRows;
   // Small grids, by the tiles that an expert of somewhat more rows than the average
-  // (their spread is about its root) needs. Up to a tile of 64 x 64 a CU: those
-  // (one expert of 96 rows, 4096 x 4096: 17 us against 20 with a ring). Up to two and
-  // a little: with a ring of four buffers (8 experts, 4096 x 4096: 16 rows 25 against
-  // 29, 48 rows 26 against 30 with rings of 128). Up to one of 128 x 128 a CU: a ring
-  // of those (64 rows 30 against 36 to 43, 96 rows 31 against 37; 7 experts of 476
-  // rows, 1040 x 776: 13.2 against 13.9; 128 rows, where many have two tiles, 55
-  // against 43 without a ring)
+  // (their spread is about its root; one alone has as many as there are) needs. Up to a
+  // tile of 64 x 64 a CU: those (one expert of 96 rows, 4096 x 4096: 17 us against 20
+  // with a ring). Up to two: with a ring of four buffers (8 experts, 4096 x 4096: 16 rows
+  // 25 against 29, 48 rows 26 against 30 with rings of 128; one expert of 512 rows 26
+  // against 30). Up to one of 128 x 128 a CU: a ring of those (64 rows 30 against 36 to 43,
+  // 96 rows 31 against 37; 7 experts of 476 rows, 1040 x 776: 13.2 against 13.9; one expert
+  // of 1024 rows 30 against 41; 128 rows, where many have two tiles, 55 against 43
+  // without a ring). Past these counts some CUs have a tile more than the others, and
+  // most grids lose by it: at two tiles of 64 and a quarter, 36 experts of 30 rows, 2048 x
+  // 1024, 27 against 22, 9 of 50 rows, 7168 x 4096, 76 against 72 (4096 x 4096 44 against
+  // 47); at one of 128 and an eighth, 9 of 100 rows, 4096 x 4096, 57 against 52, 2048 x
+  // 4096, 34 against 30.
   int64_t root = 0;
   while (root * root < rows) ++root;
-  const int64_t more = rows + root, limit = (int64_t)num_cus * 23 / 20;
-  const int64_t tiles64 = (more + 63) / 64 * ((N + 63) / 64) * d.E;
-  if (tiles64 <= num_cus) return Kernel::kTile64;
-  if (tiles64 <= 2 * limit) return Kernel::kRing64;
-  if ((more + 127) / 128 * ((N + 127) / 128) * d.E <= limit) return Kernel::kRing128;
+  const int64_t more = rows + root, most = d.E == 1 ? rows : more;
+  const int64_t ct64 = (N + 63) / 64 * d.E, ct128 = (N + 127) / 128 * d.E;
+  if ((more + 63) / 64 * ct64 <= num_cus) return Kernel::kTile64;
+  if ((most + 63) / 64 * ct64 <= 2 * num_cus) return Kernel::kRing64;
+  if ((most + 127) / 128 * ct128 <= num_cus) return Kernel::kRing128;
   // up to 40 rows tiles of 64 x 128, three buffers, weights past the caches: 8 rows 62
   // us against 68 with tiles of 128, 32 rows 74 against 81, 40 rows 77 against 83, 56
   // rows 97 against 88 (64 experts, 7168 x 4096: 39 rows 326 against 341, 47 rows 354
