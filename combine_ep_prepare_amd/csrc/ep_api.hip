@@ -522,7 +522,7 @@ ep_status_t ep_rms_norm(const ep_layout_t* layout, const void* x, const void* re
   st = current_device(&num_cus);
   if (st != EP_OK) return st;
   const NormArgs a{x, residual, weight, sum, out, out_q, out_scales, eps};
-  return launch_rms_norm(d, a, num_cus, stream) == hipSuccess ? EP_OK : EP_ERR_HIP;
+  return launch_rms_norm(d, a, stream) == hipSuccess ? EP_OK : EP_ERR_HIP;
 }
 
 size_t ep_rms_norm_bwd_workspace(const ep_layout_t* layout) {
@@ -552,7 +552,7 @@ ep_status_t ep_rms_norm_bwd(const ep_layout_t* layout, const void* grad, const v
   const NormBwdArgs a{grad,   grad_sum,    x,
                       weight, grad_x,      grad_weight,
                       static_cast<float*>(workspace), eps};
-  return launch_rms_norm_bwd(d, a, num_cus, stream) == hipSuccess ? EP_OK : EP_ERR_HIP;
+  return launch_rms_norm_bwd(d, a, stream) == hipSuccess ? EP_OK : EP_ERR_HIP;
 }
 
 ep_status_t ep_swiglu_scaled(const ep_layout_t* layout, const void* handle_mem,

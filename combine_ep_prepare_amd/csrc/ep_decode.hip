@@ -29,15 +29,11 @@
 
 #include "ep_choice.h"
 #include "ep_experts.h"
+#include "ep_matrix.h"
 
 namespace epmi {
 
 namespace {
-
-typedef float f32x4 __attribute__((ext_vector_type(4)));
-typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
-typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
-typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
 
 constexpr int kWaves = 4;             // wavefronts of a block: they split k
 constexpr int kThreads = kWaves * kWave;
@@ -45,17 +41,6 @@ constexpr int kNF = 4;                // 16-column blocks of a wavefront
 constexpr int kCols = 16 * kNF;       // columns of a tile
 constexpr int kRowTile = 16;          // rows of a tile
 constexpr int kLdsRow = kCols + 4;    // floats of a row of kCols in LDS
-
-template <int DT>
-__device__ __forceinline__ f32x4 mma16(row16_t n, row16_t m, f32x4 acc) {
-  if constexpr (DT == EP_DTYPE_BF16) {
-    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(
-        __builtin_bit_cast(bf16x8, n), __builtin_bit_cast(bf16x8, m), acc, 0, 0, 0);
-  } else {
-    return __builtin_amdgcn_mfma_f32_16x16x32_f16(
-        __builtin_bit_cast(f16x8, n), __builtin_bit_cast(f16x8, m), acc, 0, 0, 0);
-  }
-}
 
 // B in both halves of a word, and the place of the four bits in a half.
 template <int DT>

@@ -1,5 +1,6 @@
 // ep_experts.h -- device helpers of the kernels that work on the expert
-// segments of a receive buffer (ep_linear.hip, ep_decode.hip, ep_swiglu.hip):
+// segments of a receive buffer (ep_linear.hip, ep_decode.hip, ep_scaled.hip,
+// ep_swiglu.hip), and of those around it (ep_norm.hip, ep_layer.hip):
 // the live rows of a segment, the list of row tiles over all segments, and
 // the zero rows of an output of any width.
 #pragma once

@@ -183,7 +183,7 @@ __global__ void __launch_bounds__(WAVES* kWave)
         any = true;
       }
       *reinterpret_cast<u32x2*>(static_cast<uint16_t*>(a.result) + (int64_t)t * H + c) =
-          round_four<DT>(sum);
+          round4<DT>(sum);
     }
   };
   if constexpr (!UP) {
@@ -310,7 +310,7 @@ __global__ void __launch_bounds__(WAVES* kWave)
             a.act_exps[route * exps_row + cur.n0 / kExpGroup] = (uint8_t)e;
         }
         if (there) {
-          const u32x2 high = round_four<DT>(o);
+          const u32x2 high = round4<DT>(o);
           f32x4 rest;
           static_for<4>([&](auto k) {
             const uint32_t bits = (high[k.value / 2] >> (k.value % 2 * 16)) & 0xFFFFu;
@@ -320,7 +320,7 @@ __global__ void __launch_bounds__(WAVES* kWave)
           });
           uint16_t* act = static_cast<uint16_t*>(a.act) + at;
           *reinterpret_cast<u32x2*>(act) = high;
-          *reinterpret_cast<u32x2*>(act + (int64_t)n * I) = round_four<DT>(rest);
+          *reinterpret_cast<u32x2*>(act + (int64_t)n * I) = round4<DT>(rest);
         }
       } else if (there) {
         put_product(a.y + at, S::template sum_of<WAVES>(mem, m, c) +

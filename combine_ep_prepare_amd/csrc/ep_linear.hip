@@ -18,20 +18,13 @@ namespace epmi {
 
 namespace {
 
-typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
-typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
-
 // One fragment of 16 rows (or columns) of an operand for a lane: 16 bytes, 8
 // (16-bit types) or 4 (fp32) values of k. The order of k inside a fragment
 // is the same for both operands, which is all that the sum needs.
 template <int DT>
 __device__ __forceinline__ void mma(f32x4& acc, row16_t n, row16_t m) {
-  if constexpr (DT == EP_DTYPE_BF16) {
-    acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
-        __builtin_bit_cast(bf16x8, n), __builtin_bit_cast(bf16x8, m), acc, 0, 0, 0);
-  } else if constexpr (DT == EP_DTYPE_FP16) {
-    acc = __builtin_amdgcn_mfma_f32_16x16x32_f16(
-        __builtin_bit_cast(f16x8, n), __builtin_bit_cast(f16x8, m), acc, 0, 0, 0);
+  if constexpr (DT != EP_DTYPE_FP32) {
+    acc = mma16<DT>(n, m, acc);
   } else {
     static_for<4>([&](auto t) {
       acc = __builtin_amdgcn_mfma_f32_16x16x4f32(__uint_as_float(n[t.value]),

@@ -19,31 +19,26 @@
 
 #include "ep_experts.h"
 #include "ep_gate.h"
+#include "ep_matrix.h"
 #include "ep_quantise.h"
 
 namespace epmi {
 
 namespace {
 
-// Adds two sums over the block's WAVES wavefronts (over the wavefront for one).
-template <int WAVES>
-__device__ __forceinline__ void row_sums(float& a, float& b, float* lds) {
+// Adds N sums over the block's WAVES wavefronts (over the wavefront for one).
+template <int WAVES, int N>
+__device__ __forceinline__ void row_sums(float (&sums)[N], float* lds) {
   static_for<6>([&](auto i) {
-    a += __shfl_xor(a, 1 << i, kWave);
-    b += __shfl_xor(b, 1 << i, kWave);
+    static_for<N>([&](auto n) { sums[n] += __shfl_xor(sums[n], 1 << i, kWave); });
   });
   if constexpr (WAVES > 1) {
     const int wave = threadIdx.x / kWave;
-    if (lane_id() == 0) {
-      lds[wave] = a;
-      lds[WAVES + wave] = b;
-    }
+    if (lane_id() == 0) static_for<N>([&](auto n) { lds[n * WAVES + wave] = sums[n]; });
     __syncthreads();
-    a = 0.f;
-    b = 0.f;
+    static_for<N>([&](auto n) { sums[n] = 0.f; });
     static_for<WAVES>([&](auto w) {
-      a += lds[w];
-      b += lds[WAVES + w];
+      static_for<N>([&](auto n) { sums[n] += lds[n * WAVES + w]; });
     });
   }
 }
@@ -62,7 +57,7 @@ __global__ void __launch_bounds__(threads_of_block(WAVES))
   using P = Payload<DT>;
   constexpr int N = P::N;
   constexpr int kLanes = kScaleBlock / N;   // lanes that hold a block of values
-  __shared__ float lds[2 * WAVES];
+  __shared__ float lds[WAVES];
   const int t = WAVES == 1 ? lane_id() : (int)threadIdx.x;
   const int64_t row = WAVES == 1 ? (int64_t)blockIdx.x * 4 + threadIdx.x / kWave
                                  : (int64_t)blockIdx.x;
@@ -100,15 +95,15 @@ __global__ void __launch_bounds__(threads_of_block(WAVES))
       if (v < V) store_stream16(static_cast<row16_t*>(a.sum) + row * V + v, s[i]);
     });
   }
-  float ss = 0.f, none = 0.f;
+  float ss[1] = {0.f};
   static_for<VPT>([&](auto i) {
     static_for<N>([&](auto j) {
       const float f = P::template get<j>(s[i]);
-      ss = __builtin_fmaf(f, f, ss);
+      ss[0] = __builtin_fmaf(f, f, ss[0]);
     });
   });
-  row_sums<WAVES>(ss, none, lds);
-  const float r = inverse_rms(ss, d.H, a.eps);
+  row_sums<WAVES>(ss, lds);
+  const float r = inverse_rms(ss[0], d.H, a.eps);
   static_for<VPT>([&](auto i) {
     const int v = i * (WAVES * kWave) + t;
     float y[N];
@@ -169,19 +164,19 @@ __global__ void __launch_bounds__(threads_of_block(WAVES))
         if (a.grad_sum) m[i] = __builtin_nontemporal_load(more + v);
       }
     });
-    float ss = 0.f, dot = 0.f;
+    float sums[2] = {0.f, 0.f};   // of s^2, and of grad * w * s
     static_for<VPT>([&](auto i) {
       static_for<N>([&](auto j) {
         const float f = P::template get<j>(s[i]);
-        ss = __builtin_fmaf(f, f, ss);
-        dot = __builtin_fmaf(P::template get<j>(g[i]) * P::template get<j>(w[i]), f, dot);
+        sums[0] = __builtin_fmaf(f, f, sums[0]);
+        sums[1] = __builtin_fmaf(P::template get<j>(g[i]) * P::template get<j>(w[i]), f, sums[1]);
       });
     });
     // two places in turn: a wavefront may be a row ahead of another
-    row_sums<WAVES>(ss, dot, lds + turn * 2 * WAVES);
+    row_sums<WAVES>(sums, lds + turn * 2 * WAVES);
     turn ^= 1;
-    const float r = inverse_rms(ss, d.H, a.eps);
-    const float c = dot * r / (float)d.H;   // mean(grad * w * n)
+    const float r = inverse_rms(sums[0], d.H, a.eps);
+    const float c = sums[1] * r / (float)d.H;   // mean(grad * w * n)
     static_for<VPT>([&](auto i) {
       const int v = i * (WAVES * kWave) + t;
       float o[N];
@@ -228,7 +223,6 @@ __global__ void __launch_bounds__(threads_of_block(WAVES))
 // The partial weight gradients added up, in an order that the sizes alone fix:
 // a block has 16 columns, lanes of four, 256 rows at a time.
 constexpr int kSumThreads = 1024, kSumCols = 16;
-typedef float f32x4 __attribute__((ext_vector_type(4)));
 template <int DT>
 __global__ void __launch_bounds__(kSumThreads)
     norm_weight_sum_kernel(const float* __restrict__ partial, int64_t rows, int64_t H,
@@ -294,7 +288,7 @@ int64_t bwd_blocks(const Dims& d, int rows) {
 
 }  // namespace
 
-hipError_t launch_rms_norm(const Dims& d, const NormArgs& a, int, hipStream_t stream) {
+hipError_t launch_rms_norm(const Dims& d, const NormArgs& a, hipStream_t stream) {
   return with_payload(d.dtype, [&](auto dt) {
     return with_row<decltype(dt)::value, false>(d.V, [&](auto waves, auto vpt) {
       constexpr int W = decltype(waves)::value;
@@ -341,7 +335,7 @@ int64_t norm_bwd_partials(const Dims& d) {
   return n;
 }
 
-hipError_t launch_rms_norm_bwd(const Dims& d, const NormBwdArgs& a, int, hipStream_t stream) {
+hipError_t launch_rms_norm_bwd(const Dims& d, const NormBwdArgs& a, hipStream_t stream) {
   return with_payload(d.dtype, [&](auto dt) {
     constexpr int DT = decltype(dt)::value;
     hipError_t e = with_row<DT, true>(d.V, [&](auto waves, auto vpt) {

@@ -2,7 +2,7 @@
 // of a row (weights: for every 128 x 128), and the launchers of the kernels that
 // make and use them and of the ones around them (norm, layer for a few tokens).
 //
-//   scale = max(amax, 448 * 2^-100) / 448,  q = e4m3(y * (448 / max(amax, ...)))
+//   scale = max(amax, 448 * 2^-100) / 448,  q = e4m3(y * (1 / scale))
 //
 // amax is that of a block's finite values: an infinity or NaN becomes a NaN of
 // its own place and leaves its neighbours as they are. 448 is e4m3's largest
@@ -30,7 +30,7 @@ struct NormArgs {
   float* out_scales;
   float eps;
 };
-hipError_t launch_rms_norm(const Dims& d, const NormArgs& a, int num_cus, hipStream_t stream);
+hipError_t launch_rms_norm(const Dims& d, const NormArgs& a, hipStream_t stream);
 
 struct NormBwdArgs {
   const void* grad;
@@ -45,8 +45,7 @@ struct NormBwdArgs {
 // Rows of partial weight gradients: one for each block, a number that the layout
 // alone fixes.
 int64_t norm_bwd_partials(const Dims& d);
-hipError_t launch_rms_norm_bwd(const Dims& d, const NormBwdArgs& a, int num_cus,
-                               hipStream_t stream);
+hipError_t launch_rms_norm_bwd(const Dims& d, const NormBwdArgs& a, hipStream_t stream);
 
 // The gated activation with its result in 8 bits (ep_swiglu.hip).
 hipError_t launch_swiglu_scaled(const Dims& d, const HandleView& hv, const void* gate_up,

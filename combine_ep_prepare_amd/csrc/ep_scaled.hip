@@ -116,7 +116,7 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerCU)
     const int m = threadIdx.x / (kCols / 4), n = threadIdx.x % (kCols / 4) * 4;
     if (m < cur.rows && n < cur.cols)
       *reinterpret_cast<u32x2*>(out + cur.out + m * N + n) =
-          round_four<DT>(S::template sum_of<kWaves>(mem, m, n));
+          round4<DT>(S::template sum_of<kWaves>(mem, m, n));
     __syncthreads();  // the sums are read before the next tile's weights
   }
   write_zero_rows(hh, hv, d, out, N * 2 / 16);
@@ -128,6 +128,36 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerCU)
 // (14336 x 4096: 1670, 1671, 1736, 1751; a share of 32 experts, 7168 x 4096: 928, 924,
 // 916, 915).
 constexpr int kGroup = 4;
+
+// Where tile t lies: t counts an expert's tiles in groups of kGroup row tiles, each
+// column of a group after the other, and rows are shared out evenly over a segment's
+// row tiles, in blocks of 16.
+struct TilePlace {
+  int e;
+  int32_t rows, cols;    // of the tile
+  int64_t row, n0;       // the first of them
+};
+template <int BN>
+__device__ __forceinline__ TilePlace place_of(const HandleView& hv, const Dims& d,
+                                              const int32_t* tile_start, int64_t t, int32_t ct,
+                                              int64_t N) {
+  TilePlace p;
+  p.e = __builtin_amdgcn_readfirstlane(expert_of_tile(tile_start, d.E, (int32_t)(t / ct)));
+  const int32_t rts = tile_start[p.e + 1] - tile_start[p.e];
+  const int64_t in_e = t - (int64_t)tile_start[p.e] * ct;
+  const int32_t group = (int32_t)(in_e / ((int64_t)kGroup * ct));
+  const int32_t in_g = (int32_t)(in_e - (int64_t)group * kGroup * ct);
+  const int32_t gm = rts - group * kGroup < kGroup ? rts - group * kGroup : kGroup;
+  const int32_t mi = __builtin_amdgcn_readfirstlane(group * kGroup + in_g % gm);
+  p.n0 = __builtin_amdgcn_readfirstlane((in_g / gm) * BN);
+  const Segment s = segment_of(hv, d, p.e);
+  const int32_t height = (int32_t)((((int64_t)s.rows + rts - 1) / rts + 15) / 16 * 16);
+  const int64_t m0 = (int64_t)mi * height;
+  p.rows = (int32_t)(s.rows - m0 < height ? s.rows - m0 : height);
+  p.cols = (int32_t)(N - p.n0 < BN ? N - p.n0 : BN);
+  p.row = s.row + m0;
+  return p;
+}
 
 // Many rows: the tiled product of ep_linear.hip with steps of 128 values of k, one
 // block of scales each. WM x WN wavefronts hold every WM-th block of 16 rows and
@@ -203,22 +233,11 @@ __global__ void __launch_bounds__(WM* WN* kWave)
     // have: opaque here and below, it is worked out for each tile.
     int32_t ct = all_ct, H = all_H;
     asm volatile("" : "+s"(ct), "+s"(H));
-    const int e = __builtin_amdgcn_readfirstlane(
-        expert_of_tile(tile_start, d.E, (int32_t)(t / ct)));
-    const int32_t rts = tile_start[e + 1] - tile_start[e];
-    const int64_t in_e = t - (int64_t)tile_start[e] * ct;
-    const int32_t group = (int32_t)(in_e / ((int64_t)kGroup * ct));
-    const int32_t in_g = (int32_t)(in_e - (int64_t)group * kGroup * ct);
-    const int32_t gm = rts - group * kGroup < kGroup ? rts - group * kGroup : kGroup;
-    const int32_t mi = __builtin_amdgcn_readfirstlane(group * kGroup + in_g % gm);
-    const int64_t n0 = __builtin_amdgcn_readfirstlane((in_g / gm) * BN);
-    const Segment s = segment_of(hv, d, e);
-    // rows are shared out evenly over a segment's tiles, in blocks of 16
-    const int32_t height = (int32_t)((((int64_t)s.rows + rts - 1) / rts + 15) / 16 * 16);
-    const int64_t m0 = (int64_t)mi * height;
-    const int32_t mrows = (int32_t)(s.rows - m0 < height ? s.rows - m0 : height);
-    const int32_t ncols = (int32_t)(N - n0 < BN ? N - n0 : BN);
-    const char* a_src = reinterpret_cast<const char*>(x) + (s.row + m0) * H;
+    const TilePlace at = place_of<BN>(hv, d, tile_start, t, ct, N);
+    const int e = at.e;
+    const int64_t row = at.row, n0 = at.n0;
+    const int32_t mrows = at.rows, ncols = at.cols;
+    const char* a_src = reinterpret_cast<const char*>(x) + row * H;
     const char* b_src = reinterpret_cast<const char*>(w) + ((int64_t)e * N + n0) * H;
     uint32_t a_off[2][AL], b_off[BL];
     static_for<AL>([&](auto i) {
@@ -264,7 +283,7 @@ __global__ void __launch_bounds__(WM* WN* kWave)
     const uint32_t s_off = (uint32_t)(wave * kShare + lane) * (uint32_t)(SX * 4);
     auto load_scales = [&](int j) {
       const uint32_t bytes = (uint32_t)mrows * (uint32_t)(SX * 4);
-      load_to_lds<false, 0>(buffer_of(x_scales + (s.row + m0) * SX, bytes),
+      load_to_lds<false, 0>(buffer_of(x_scales + row * SX, bytes),
                             j * 4 < SX ? s_off + (uint32_t)j * 16 : kOutside,
                             __builtin_amdgcn_readfirstlane(scale_base + (j & 1) * kScaleBytes +
                                                            wave * kShare * 16));
@@ -429,7 +448,7 @@ __global__ void __launch_bounds__(WM* WN* kWave)
       asm volatile("" : "+v"(place));
       static_for<MF>([&](auto i) {
         const int32_t m = (i * WM + wm) * 16 + (place & 15);
-        uint16_t* to = out + (s.row + m0 + m) * N + n0;
+        uint16_t* to = out + (row + m) * N + n0;
         static_for<NF / 2>([&](auto j) {
           const row16_t v = round_and_join<DT>(acc[i][2 * j], acc[i][2 * j + 1]);
           const int32_t n = wn * (BN / WN) + j * 32 + (place >> 4) * 8;
@@ -513,23 +532,13 @@ __global__ void __launch_bounds__(WM* WN* kWave)
   const int64_t slots = gridDim.x / kRunXcds;
   const int64_t xcd = blockIdx.x % kRunXcds, slot = blockIdx.x / kRunXcds;
   for (int64_t t = xcd * slots + slot; t < tiles; t += gridDim.x) {
-    const int e = __builtin_amdgcn_readfirstlane(
-        expert_of_tile(tile_start, d.E, (int32_t)(t / ct)));
-    const int32_t rts = tile_start[e + 1] - tile_start[e];
-    const int64_t in_e = t - (int64_t)tile_start[e] * ct;
-    const int32_t group = (int32_t)(in_e / ((int64_t)kGroup * ct));
-    const int32_t in_g = (int32_t)(in_e - (int64_t)group * kGroup * ct);
-    const int32_t gm = rts - group * kGroup < kGroup ? rts - group * kGroup : kGroup;
-    const int32_t mi = __builtin_amdgcn_readfirstlane(group * kGroup + in_g % gm);
-    const int64_t n0 = __builtin_amdgcn_readfirstlane((in_g / gm) * BN);
-    const Segment s = segment_of(hv, d, e);
-    const int32_t height = (int32_t)((((int64_t)s.rows + rts - 1) / rts + 15) / 16 * 16);
-    const int64_t m0 = (int64_t)mi * height;
-    const int32_t mrows = (int32_t)(s.rows - m0 < height ? s.rows - m0 : height);
-    const int32_t ncols = (int32_t)(N - n0 < BN ? N - n0 : BN);
-    const char* a_src = reinterpret_cast<const char*>(x) + (s.row + m0) * H;
+    const TilePlace at = place_of<BN>(hv, d, tile_start, t, ct, N);
+    const int e = at.e;
+    const int64_t row = at.row, n0 = at.n0;
+    const int32_t mrows = at.rows, ncols = at.cols;
+    const char* a_src = reinterpret_cast<const char*>(x) + row * H;
     const char* b_src = reinterpret_cast<const char*>(w) + ((int64_t)e * N + n0) * H;
-    const float* s_src = x_scales + (s.row + m0) * SX;
+    const float* s_src = x_scales + row * SX;
     uint32_t a_off[AL], b_off[BL];
     static_for<AL>([&](auto i) { a_off[i] = A::source(wave * AL + i, (uint32_t)H, 0); });
     static_for<BL>([&](auto i) { b_off[i] = B::source(wave * BL + i, (uint32_t)H, 0); });
@@ -607,7 +616,7 @@ __global__ void __launch_bounds__(WM* WN* kWave)
     if (busy) {
       static_for<MF>([&](auto i) {
         const int32_t m = (i * WM + wm) * 16 + (lane & 15);
-        uint16_t* to = out + (s.row + m0 + m) * N + n0;
+        uint16_t* to = out + (row + m) * N + n0;
         static_for<NF / 2>([&](auto j) {
           const row16_t v = round_and_join<DT>(acc[i][2 * j], acc[i][2 * j + 1]);
           const int32_t n = wn * (BN / WN) + j * 32 + (lane >> 4) * 8;

@@ -1,16 +1,15 @@
 // ep_tiles.h -- what the tiled products have in common (ep_linear.hip,
 // ep_scaled.hip): loads from global memory straight into LDS, the layout of an
-// operand's tile there, and the rounding and joining of results.
+// operand's tile there, and the joining of results.
 #pragma once
 
 #include "ep_experts.h"
+#include "ep_matrix.h"
 
 namespace epmi {
 
 namespace {
 
-typedef float f32x4 __attribute__((ext_vector_type(4)));
-typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
 typedef short s16x4 __attribute__((ext_vector_type(4)));
 typedef short s16x8 __attribute__((ext_vector_type(8)));
 
@@ -150,17 +149,6 @@ struct Operand {
     }
   }
 };
-
-// Four results rounded to 16 bits.
-template <int DT>
-__device__ __forceinline__ u32x2 round4(f32x4 v) {
-  if constexpr (DT == EP_DTYPE_BF16) {
-    return u32x2{rne_bf16(v[0]) | (rne_bf16(v[1]) << 16),
-                 rne_bf16(v[2]) | (rne_bf16(v[3]) << 16)};
-  } else {
-    return u32x2{rne_f16(v[0]) | (rne_f16(v[1]) << 16), rne_f16(v[2]) | (rne_f16(v[3]) << 16)};
-  }
-}
 
 // A lane of quarter q holds columns 4 q to 4 q + 3 of two neighbouring blocks
 // of 16, and gets columns 8 q to 8 q + 7 of the 32: stores of 16 bytes, 64 to a
