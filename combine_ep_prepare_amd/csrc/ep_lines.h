@@ -85,8 +85,8 @@ __device__ __forceinline__ float inverse_power_of(uint32_t exponent) {
 // an fp16 number down to 2^-44, where nothing is left of a value.
 __device__ __forceinline__ row16_t lower8(row16_t v, int by) {
   by = by > -44 ? by : -44;
-  const _Float16 f0 = (_Float16)__uint_as_float((uint32_t)(127 + by / 2) << 23);
-  const _Float16 f1 = (_Float16)__uint_as_float((uint32_t)(127 + by - by / 2) << 23);
+  const _Float16 f0 = __builtin_amdgcn_ldexph((_Float16)1.f, by >> 1);
+  const _Float16 f1 = __builtin_amdgcn_ldexph((_Float16)1.f, by - (by >> 1));
   f16x8 h = __builtin_bit_cast(f16x8, v);
   h = h * f0 * f1;
   return __builtin_bit_cast(row16_t, h);
