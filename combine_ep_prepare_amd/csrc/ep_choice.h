@@ -82,10 +82,10 @@ inline Kernel kernel_of(Product p, const Dims& d, int64_t N, int num_cus) {
 // 128 experts, 2048 inputs and 1536 outputs unless another size is named.
 inline Kernel scaled_kernel_of(const Dims& d, int64_t N, int num_cus) {
   const int64_t rows = most_rows(d) / d.E;
-  // up to 6 rows: 6 rows 64 us against 65 with the tiles below, 2 rows 55 against 60;
-  // 8 rows 68 against 62. One expert's few tiles leave most CUs without work, so that
-  // up to 32 rows those of 16 are ahead (4096 x 4096: 32 rows 12 against 17, 64 rows
-  // 18 against 17)
+  // up to 6 rows: 2 rows 57 us against 62 with the tiles below, 6 rows 66 against 65;
+  // 8 rows 67 against 64. One expert's few tiles leave most CUs without work, so that
+  // up to 32 rows those of 16 are ahead (4096 x 4096: 32 rows 14 against 17, 64 rows
+  // 17 against 18)
   if (rows <= 6 || (d.E == 1 && rows <= 32)) return Kernel::kFewRows;
   // Small grids, by the tiles that an expert of somewhat more rows than the average
   // (their spread is about its root; one alone has as many as there are) needs. Up to a
@@ -119,9 +119,9 @@ inline Kernel scaled_kernel_of(const Dims& d, int64_t N, int num_cus) {
   // against 78, 128 rows 50 against 43).
   const int64_t tiles256 = (rows + 255) / 256 * ((N + 255) / 256) * d.E;
   if ((rows > 104 || d.H >= 4096) && tiles256 >= (rows > 128 ? num_cus / 2 : num_cus)) {
-    // the weights past the caches while most experts have one row tile: 160 rows 112
-    // us against 120, 192 rows 117 against 127; 256 rows of 8 experts 62 against 60,
-    // 4096 rows of 8 (4096 x 28672) 4700 against 4040
+    // the weights past the caches while most experts have one row tile: 160 rows 119
+    // us against 127, 192 rows 125 against 132, 224 rows still 151 against 160; 256 rows
+    // of 8 experts 66 against 60, 4096 rows of 8 (4096 x 28672) 3645 against 3500
     return rows <= 192 ? Kernel::kTile256Once : Kernel::kTile256;
   }
   // weights past the caches up to 104 rows: 48 rows 87 us against 91, 96 rows 92

@@ -264,8 +264,11 @@ hipError_t with_row(int64_t V, F&& f) {
   if (V <= 256) return f(integral_constant<int, 1>{}, integral_constant<int, 4>{});
   if (V <= 512) return f(integral_constant<int, 4>{}, integral_constant<int, 2>{});
   if (V <= 1024) {
-    // eight wavefronts, 32768 rows of 7168 bf16 values with a residual, in 8 bits: 268
-    // us against 276 with four; backward, where the weight's sums are a lane's too, four
+    // eight wavefronts, against four; 32768 rows of bf16 values with a residual, in 8
+    // bits: 7168 values 271 us against 276, 8192 313 against 319, 6144 230 against 236,
+    // but 5120 199 against 197 and 4224 183 against 166, where a lane's second
+    // vector mostly lies past the row; 16 rows of 5120 4.3 against 5.2, of 7168 4.6 against 5.6; fp32, 16384 rows
+    // of 4096, 141 against 142. Backward, where the weight's sums are a lane's too, four
     if constexpr (!BWD) return f(integral_constant<int, 8>{}, integral_constant<int, 2>{});
     return f(integral_constant<int, 4>{}, integral_constant<int, 4>{});
   }
@@ -276,10 +279,14 @@ hipError_t with_row(int64_t V, F&& f) {
 }
 
 // Blocks of the backward pass, two a CU: each writes its part of the weight
-// gradient. 16384 rows of 4096 bf16 values with a gradient of the sum: 98 us,
-// against 103 with 768, 111 with 1024 (whose parts are 17 MB more to write and
-// read) and 115 with 2048; with the next row's loads ahead of this one's sums 99
-// (106 with 256).
+// gradient. bf16 rows with a gradient of the sum, us with 512 blocks, and with 256,
+// 1024 and 2048, whose parts are more bytes to write and read:
+//   16384 x 4096    92   136  105  109       65536 x 1024     95   122  100  102
+//   16384 x 7168   168   223  176  186       131072 x 512    110   192   98  102
+//   8192 x 14336   179   173  193  223       262144 x 256    193   353  131  125
+//   2048 x 4096     24    26   28   35       524288 x 64     351   671  217  201
+// Narrow rows, one a wavefront, are few bytes in flight in 512 blocks: more would serve
+// many of them better. fp32, 16384 x 4096: 183, 199, 191, 193.
 constexpr int64_t kBwdBlocks = 512;
 int64_t bwd_blocks(const Dims& d, int rows) {
   const int64_t blocks = (d.T + rows - 1) / rows;

@@ -124,9 +124,9 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerCU)
 
 // Row tiles of an expert whose column tiles run together: with the columns
 // dealt after them, the tiles in flight on an XCD share both operands. 8 experts of
-// 4096 rows, 4096 x 28672: 3530 us, against 3577 with 8, 3636 with 6 and 3645 with 12
-// (14336 x 4096: 1670, 1671, 1736, 1751; a share of 32 experts, 7168 x 4096: 928, 924,
-// 916, 915).
+// 4096 rows, 4096 x 28672: 3495 us, against 3545 with 8, 3600 with 6 and 3635 with 12
+// (14336 x 4096: 1700, 1710, 1787, 1790; a share of 32 experts of 1024 rows, 7168 x
+// 4096, within 2%).
 constexpr int kGroup = 4;
 
 // Where tile t lies: t counts an expert's tiles in groups of kGroup row tiles, each
@@ -171,11 +171,13 @@ __device__ __forceinline__ TilePlace place_of(const HandleView& hv, const Dims& 
 // bytes a row; the columns' one of a step is the same for a wavefront, whose columns
 // lie in one block.
 //
-// 8 experts of 4096 rows: 2200 TFLOP/s at 4096 x 28672, 2340 at 14336 x 4096 (a
+// 8 experts of 4096 rows: 2200 TFLOP/s at 4096 x 28672, 2270 at 14336 x 4096 (a
 // library product of 8-bit operands without scales 3000). The clock falls to 1.6 GHz
-// on random operands (2650 TFLOP/s on zeros), and the matrix units are busy 53% of
-// its cycles: two wavefronts a SIMD leave them idle around the syncs, and the
-// multiply-adds take a tenth (2350 TFLOP/s without). More than 256 registers a
+// on random operands (2650 TFLOP/s on zeros), and the matrix units are busy 53% of its
+// cycles: power is not all of it. Two wavefronts a SIMD leave them idle around the
+// syncs, and of seven vector instructions a matrix product four are the multiply-adds
+// (2350 TFLOP/s without) and two to three work out offsets and buffers of the next
+// loads anew each step, for an end that the last step alone has. More than 256 registers a
 // wavefront would let a larger part read less from LDS, but only instructions of the
 // matrix unit reach the second half of the file, and the sums need others. 32 x 32 x
 // 64 instructions, whose 16 sums a lane spill, ran at 1970.

@@ -102,9 +102,11 @@ __global__ void __launch_bounds__(kThreads)
 // side in a row: 16 (fp32: 32) neighbouring lanes hold them, 16 bytes of each
 // half a lane, and the scale's maximum takes four (five) exchanges. Rows are
 // dealt by such blocks in address order. 32768 rows of 14336 values 412 us, 5.8
-// TB/s; uneven experts' 65536 rows of 768 52. Both were bound by the arithmetic (421
-// and 61 us) while a value took 32 vector instructions, for rows of a step in 64
-// bits, a shuffle an exchange, IEEE quotients and a flag a value: it takes 22.
+// TB/s; uneven experts' 65536 rows of 768 47 to 53, by the calls around it; fp32,
+// 16384 rows of 4096 110 us, 5.5 TB/s. Both of the first were bound by the arithmetic
+// (420 and 51 us, beside 411 and 47 the same day) while a value took 32 vector
+// instructions, for rows of a step in 64 bits, a shuffle an exchange, IEEE quotients
+// and a flag a value: it takes 22.
 template <int DT>
 __global__ void __launch_bounds__(kThreads)
     swiglu_scaled_kernel(Dims d, HandleView hv, const row16_t* __restrict__ gate_up,
@@ -187,7 +189,7 @@ hipError_t launch_swiglu_scaled(const Dims& d, const HandleView& hv, const void*
                                 uint8_t* out_q, float* out_scales, int num_cus,
                                 hipStream_t stream) {
   // Short blocks, of 512 vectors or a row, each of one step: 32768 rows of 14336 values
-  // 412 us, 437 with two rows; uneven experts' rows of 768 52, and 59, 53 and 55 with
+  // 410 us, 439 with two rows; uneven experts' rows of 768 53, and 61, 54 and 56 with
   // 256, 1024 and 2048 vectors. The limit keeps the grid's threads below 2^32.
   const int32_t step_rows = (int32_t)((512 + d.V - 1) / d.V);
   int64_t blocks = (d.cap + step_rows - 1) / step_rows;
