@@ -19,23 +19,6 @@ namespace epmi {
 
 namespace {
 
-typedef int i32x8 __attribute__((ext_vector_type(8)));
-
-// A whole block of 128 e4m3 values of k at once: 32 a lane, in two halves. Of each
-// eight neighbouring products the instruction cuts off what lies 13 bits below the largest,
-// as the 16 x 16 x 32 one of 8-bit operands does: a sum of products of all sizes is off
-// by 2^-11 of the largest (measured; by 2^-20 with 16-bit operands). The tiled products
-// take it all the same, at twice the 16-bit rate (8 experts of 4096 rows, 4096 x 28672:
-// 3510 us, and 6150 with 16-bit weights); the products below widen their operands, in
-// the time that the weights' bytes take anyway.
-__device__ __forceinline__ f32x4 mma8(row16_t n0, row16_t n1, row16_t m0, row16_t m1) {
-  struct Both { row16_t a, b; };
-  const f32x4 zero = {0.f, 0.f, 0.f, 0.f};
-  return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
-      __builtin_bit_cast(i32x8, Both{n0, n1}), __builtin_bit_cast(i32x8, Both{m0, m1}), zero, 0,
-      0, 0, 0, 0, 0);
-}
-
 // Eight e4m3 values to the payload type, exactly (both types hold them all).
 template <int DT>
 __device__ __forceinline__ row16_t widen8(uint32_t lo, uint32_t hi) {
@@ -59,7 +42,8 @@ enum Form {
   kPayload,   // weights and x of the payload type
   kScaled,    // weights and x in 8 bits, each with scales; multiplied as 16-bit values,
               // with fp32 sums (32 tokens by top-8 of 256, 7168 x 4096: 691 us, 690 with
-              // mma8; one expert of 16 rows, 4096 x 4096: 10.7 against 9.9)
+              // the 8-bit instruction, which cuts them off; one expert of 16 rows, 4096 x
+              // 4096: 10.7 against 9.9)
   kWeights8   // weights in 8 bits with scales, x of the payload type: a block's
               // sum is that of the e4m3 values themselves, and scaled in fp32
 };

@@ -71,3 +71,36 @@ def test_weights_past_31_bits(eight):
     want = run(3, few_idx, w1[0], w1[1], w2[0], w2[1])
     got = run(E, idx, w1[2], w1[3], w2[2], w2[3])
     assert want.isfinite().all() and float(want.abs().max()) > 0 and torch.equal(got, want)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+@pytest.mark.parametrize("eight", [False, True])
+def test_two_graphs_share_a_workspace(eight, dtype):
+    """Captured calls of two sizes with one workspace, replayed in turn, on rows and
+    routes that change between replays."""
+    a = Layer("masked", 6, 3, 7, 272, 208, dtype, eight, seed=1)
+    b = Layer("any", 3, 5, 9, 144, 400, dtype, eight, seed=2)
+    if a.workspace.numel() < b.workspace.numel():
+        a.workspace = b.workspace
+    b.workspace = a.workspace
+    graphs, outs = [], []
+    for case in (a, b):
+        case.run()
+        out = torch.zeros_like(case.x, device="cuda")
+        torch.cuda.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            case.run(out)
+        graphs.append(graph)
+        outs.append(out)
+    gen = torch.Generator().manual_seed(5)
+    for _ in range(3):
+        for case, graph, out in zip((a, b), graphs, outs):
+            case.x = (torch.randn(case.x.shape, generator=gen) * 8).to(case.dt)
+            case.idx = case.idx[torch.randperm(case.idx.shape[0], generator=gen)].contiguous()
+            case.args[2].copy_(case.x)
+            case.args[0].copy_(case.idx)
+            out.fill_(7.0)
+            graph.replay()
+            torch.cuda.synchronize()
+            case.check(out)
