@@ -159,15 +159,17 @@ struct Lines {
     });
   }
   // The step's x to the largest of its exponents, which it returns.
-  __device__ __forceinline__ uint32_t level(row16_t (&xs)[kX], const uint32_t (&ex)[kExpWords > 0 ? kExpWords : 1]) const {
+  template <int WORDS>
+  __device__ static __forceinline__ uint32_t level(row16_t (&xs)[kX],
+                                                   const uint32_t (&ex)[WORDS]) {
     uint32_t most = 0;
-    static_for<kExpWords * 4>([&](auto i) {
+    static_for<WORDS * 4>([&](auto i) {
       const uint32_t e = (ex[i / 4] >> (i % 4 * 8)) & 0xFF;
       most = e > most ? e : most;
     });
     static_for<kX>([&](auto p) {
       const int group = input(p) / kExpGroup;
-      const uint32_t word = kExpWords > 1 && p >= kX / 2 ? ex[kExpWords - 1] : ex[0];
+      const uint32_t word = ex[p * WORDS / kX];
       const uint32_t own = (word >> (group % 4 * 8)) & 0xFF;
       xs[p] = lower8(xs[p], (int)own - (int)most);
     });

@@ -266,9 +266,10 @@ hipError_t with_row(int64_t V, F&& f) {
   if (V <= 1024) {
     // eight wavefronts, against four; 32768 rows of bf16 values with a residual, in 8
     // bits: 7168 values 271 us against 276, 8192 313 against 319, 6144 230 against 236,
-    // but 5120 199 against 197 and 4224 183 against 166, where a lane's second
-    // vector mostly lies past the row; 16 rows of 5120 4.3 against 5.2, of 7168 4.6 against 5.6; fp32, 16384 rows
-    // of 4096, 141 against 142. Backward, where the weight's sums are a lane's too, four
+    // but 5120 199 against 197 and 4224 183 against 166, where a lane's second vector
+    // mostly lies past the row; 16 rows of 5120 4.3 against 5.2, of 7168 4.6 against
+    // 5.6; fp32, 16384 rows of 4096, 141 against 142. Backward, where the weight's sums
+    // are a lane's too, four
     if constexpr (!BWD) return f(integral_constant<int, 8>{}, integral_constant<int, 2>{});
     return f(integral_constant<int, 4>{}, integral_constant<int, 4>{});
   }

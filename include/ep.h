@@ -572,11 +572,11 @@ ep_status_t ep_swiglu_scaled(const ep_layout_t* layout, const void* handle_mem,
  * Grouped linear of 8-bit operands: ep_grouped_linear of the values that x and
  * weight stand for, the scales applied in fp32 to the sums over a block, out
  * rounded once to the payload type (bf16 or fp16; fp32 is EP_ERR_SHAPE). With up to
- * six rows an expert on average (one expert: 32), as when decoding, sums are fp32.
- * With more, a block's sum is that of the 8-bit matrix instruction, which cuts
- * products off 13 bits below the largest of the eight neighbours that it adds
- * first, and fp32 from there on. For serving, with no backward. H = layout->hidden is a multiple of 16, N =
- * out_features of 8.
+ * six rows an expert (the routes T*K, or the capacity if less, over E; 32 for one
+ * expert alone), as when decoding, sums are fp32. With more, a block's sum is that of
+ * the 8-bit matrix instruction, which cuts products off 13 bits below the largest of
+ * the eight neighbours that it adds first, and fp32 from there on. For serving, with
+ * no backward. H = layout->hidden is a multiple of 16, N = out_features of 8.
  *   x              e4m3 [recv_capacity,H]
  *   x_scales       fp32 [recv_capacity, EP_SCALE_COLUMNS(H)]
  *   weight         e4m3 [E,N,H]
@@ -599,13 +599,13 @@ ep_status_t ep_grouped_linear_scaled(const ep_layout_t* layout, const void* hand
  * type, to 16 bits in bf16, and in fp16 with an exponent for every 16 values, to 22
  * bits or 2^-36 of the largest among the 64 (8-bit weights: 128) that enter the
  * products together: neither range nor subnormals of the type take anything from
- * it. An infinite weight of down may reach its outputs as NaN. A route whose id is outside [0,E),
- * masked or not, counts nothing; a token with no valid route gets +0; an expert
- * may come more than once. T*K is at most EP_MAX_LAYER_ROUTES; uses the layout's num_tokens,
- * topk, num_experts, hidden and dtype (bf16 or fp16; fp32 is EP_ERR_SHAPE). For
- * serving, with no backward. The weights are of the payload type, or, with both
- * scales given, e4m3 with 128 x 128 scales (hidden and inner multiples of 16
- * then); their values enter the products exactly and the scales the fp32 sums.
+ * it. An infinite weight of down may reach its outputs as NaN. A route whose id is
+ * outside [0,E), masked or not, counts nothing; a token with no valid route gets +0;
+ * an expert may come more than once. T*K is at most EP_MAX_LAYER_ROUTES; uses the
+ * layout's num_tokens, topk, num_experts, hidden and dtype (bf16 or fp16; fp32 is
+ * EP_ERR_SHAPE). For serving, with no backward. The weights are of the payload type,
+ * or, with both scales given, e4m3 with 128 x 128 scales (hidden and inner multiples
+ * of 16 then); their values enter the products exactly and the scales the fp32 sums.
  *   topk_idx        int64 [T,K]
  *   topk_weights    fp32 [T,K]
  *   tokens          payload [T,H]
